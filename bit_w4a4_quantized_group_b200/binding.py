@@ -19,12 +19,15 @@ SVDQ_FMT_NVFP4_G16 = 1
 SVDQ_FMT_INT4_G64 = 2
 SVDQ_FMT_MXFP4_G32 = 3
 SVDQ_FMT_W8A8 = 4
+SVDQ_FMT_FP8_G128 = 5
 FORMATS = {"nvfp4": SVDQ_FMT_NVFP4_G16, "int4": SVDQ_FMT_INT4_G64, "mxfp4": SVDQ_FMT_MXFP4_G32,
-           "w8a8": SVDQ_FMT_W8A8}
+           "w8a8": SVDQ_FMT_W8A8, "fp8": SVDQ_FMT_FP8_G128}
+SVDQ_ACT_SILU, SVDQ_ACT_GELU_TANH = 1, 2
+ACTIVATIONS = {"silu": SVDQ_ACT_SILU, "gelu": SVDQ_ACT_GELU_TANH}
 
 EXPORTED = (
     "svdq_buffer_sizes", "svdq_pack_weight", "svdq_quantize_act_lowrank_down",
-    "svdq_w4a4_gemm_lowrank_up", "svdq_status_string", "svdq_get_last_device_error",
+    "svdq_w4a4_gemm_lowrank_up", "svdq_rmsnorm_quantize_act", "svdq_glu_quantize_act", "svdq_status_string", "svdq_get_last_device_error",
     "svdq_last_launch_count", "svdq_last_cuda_error", "svdq_selftest_bounded_wait",
 )
 
@@ -59,6 +62,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.svdq_quantize_act_lowrank_down.argtypes = [c_int, i64, i64, c_int, vp, vp, f32, vp, vp, vp, vp, vp]
     lib.svdq_w4a4_gemm_lowrank_up.argtypes = [c_int, i64, i64, i64, c_int, vp, vp, f32, vp, vp, f32,
                                               vp, vp, vp, vp, vp]
+    lib.svdq_rmsnorm_quantize_act.argtypes = [c_int, i64, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, vp, vp]
+    lib.svdq_glu_quantize_act.argtypes = [c_int, c_int, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp]
     lib.svdq_status_string.argtypes = [c_int]
     lib.svdq_status_string.restype = ctypes.c_char_p
     lib.svdq_get_last_device_error.argtypes = [vp, ctypes.POINTER(c_int)]
@@ -105,6 +110,16 @@ def svdq_w4a4_gemm_lowrank_up(fmt, M, N, K, rank, a_codes, a_scales, act_gscale,
                               Z, L2, bias, Y, stream) -> int:
     return load().svdq_w4a4_gemm_lowrank_up(_fmt(fmt), M, N, K, rank, a_codes, a_scales, act_gscale, w_codes,
                                             w_scales, w_gscale, Z, L2, bias, Y, stream)
+
+
+def svdq_rmsnorm_quantize_act(fmt, M, K, X, ldx, residual, ldr, gamma, eps, H, ldh, a_codes, a_scales, stream) -> int:
+    return load().svdq_rmsnorm_quantize_act(_fmt(fmt), M, K, X, ldx, residual, ldr, gamma, eps, H, ldh, a_codes,
+                                            a_scales, stream)
+
+
+def svdq_glu_quantize_act(fmt, act, M, K, gate, ldg, up, ldu, lam, a_codes, a_scales, stream) -> int:
+    return load().svdq_glu_quantize_act(_fmt(fmt), ACTIVATIONS[act] if isinstance(act, str) else int(act), M, K,
+                                        gate, ldg, up, ldu, lam, a_codes, a_scales, stream)
 
 
 def svdq_get_last_device_error(stream=None):
@@ -182,3 +197,42 @@ def w4a4_gemm_lowrank_up_t(fmt, M, N, K, rank, a_codes, a_scales, act_gscale, w_
                                    _ptr(w_codes), _ptr(w_scales), w_gscale, _ptr(Z), _ptr(L2), _ptr(bias),
                                    _ptr(Y), _stream() if stream is None else stream)
     _check(st, "svdq_w4a4_gemm_lowrank_up")
+
+
+def _rows(t):
+    """(pointer, row stride in elements) of a [M, K] tensor with contiguous rows; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError("the elements of a row must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _same_matrix(ref, **others):
+    """Every given tensor has ref's shape, 2-byte elements like ref, and ref's device."""
+    for name, t in others.items():
+        if t is not None and (t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device):
+            raise ValueError(f"{name}: expected {tuple(ref.shape)} {ref.dtype} on {ref.device}, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def rmsnorm_quantize_act_t(fmt, X, residual, gamma, eps, H, a_codes, a_scales, stream=None):
+    """Residual addition + RMS norm + quantization on torch tensors: X, residual, H bf16 [M, K] (rows
+    may be strided; residual and H may be None), gamma fp32 [K] or None."""
+    M, K = X.shape
+    _same_matrix(X, residual=residual, H=H)
+    (x, ldx), (r, ldr), (h, ldh) = _rows(X), _rows(residual), _rows(H)
+    st = svdq_rmsnorm_quantize_act(fmt, M, K, x, ldx, r, ldr, _ptr(gamma), eps, h, ldh, _ptr(a_codes),
+                                   _ptr(a_scales), _stream() if stream is None else stream)
+    _check(st, "svdq_rmsnorm_quantize_act")
+
+
+def glu_quantize_act_t(fmt, act, gate, up, lam, a_codes, a_scales, stream=None):
+    """act(gate) [* up] [/ lam] + quantization on torch tensors: act "silu" or "gelu" (tanh form), gate
+    and up bf16 [M, K] (column slices of a wider tensor will do; up may be None), lam fp32 [K] or None."""
+    M, K = gate.shape
+    _same_matrix(gate, up=up)
+    (g, ldg), (u, ldu) = _rows(gate), _rows(up)
+    st = svdq_glu_quantize_act(fmt, act, M, K, g, ldg, u, ldu, _ptr(lam), _ptr(a_codes), _ptr(a_scales),
+                               _stream() if stream is None else stream)
+    _check(st, "svdq_glu_quantize_act")

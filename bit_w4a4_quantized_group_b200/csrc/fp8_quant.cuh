@@ -1,0 +1,83 @@
+// Device helpers of the kernels that write FP8 activations: the E8M0 scale of a 128-element
+// group, the E4M3 codes under it, and the byte layout of the scales.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "svdq_device.cuh"
+
+namespace svdq {
+
+// E8M0 byte e + 127 of the smallest e >= -127 with a <= 448 * 2^e, for a >= 0: with a = f 2^(E - 127),
+// f in [1, 2), and 448 = 1.75 * 2^8, e + 127 is E - 8, one more when f > 1.75.  Zero and subnormal
+// a have E = 0 and get byte 0.
+__device__ __forceinline__ uint32_t fp8_scale_byte(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int b = static_cast<int>(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return static_cast<uint32_t>(max(b, 0));
+}
+// 2^-e for the byte e + 127 (0..248): the exponent field 254 - byte is that of a normal number,
+// so multiplying by it divides by the scale exactly.
+__device__ __forceinline__ float fp8_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// Byte offset of (row, group) in the blocked FP8 scale layout; sfb = ceil(K/512) blocks per 128 rows.
+__device__ __forceinline__ size_t fp8_sf_offset(int row, int grp, int sfb) {
+  return (static_cast<size_t>(row >> 7) * sfb + (grp >> 2)) * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 +
+         (grp & 3);
+}
+
+__device__ __forceinline__ float bf16x2_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16x2_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// 16 bytes that are read once: no line is kept in L1.  A plain load, not the read-only path: the
+// same thread may later write to the address (an output in place).
+__device__ __forceinline__ uint4 ld_global_v4_na(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// Maximum over the 16 lanes that hold one group (8 elements each).
+__device__ __forceinline__ float group_max16(float a) {
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
+  return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
+}
+__device__ __forceinline__ float max8(const float (&y)[8]) {
+  return fmaxf(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))),
+               fmaxf(fmaxf(fabsf(y[4]), fabsf(y[5])), fmaxf(fabsf(y[6]), fabsf(y[7]))));
+}
+
+// Codes and scale of this thread's 8 elements (chunk c of the row) of a group that 16 lanes hold;
+// all lanes of the warp call it, `on` says whether the lane has a chunk (whole groups at a time).
+__device__ __forceinline__ void fp8_store_chunk(const float (&y)[8], bool on, int row, int c, int K, int sfb,
+                                                uint8_t* codes, uint8_t* scales, size_t nscale, int* err) {
+  const float a = group_max16(on ? max8(y) : 0.f);
+  const uint32_t b = fp8_scale_byte(a);
+  const float inv = fp8_inv_scale(b);
+  uint2 q;
+  q.x = ptx::cvt_e4m3x2(y[0] * inv, y[1] * inv) | (ptx::cvt_e4m3x2(y[2] * inv, y[3] * inv) << 16);
+  q.y = ptx::cvt_e4m3x2(y[4] * inv, y[5] * inv) | (ptx::cvt_e4m3x2(y[6] * inv, y[7] * inv) << 16);
+  if (on && SVDQ_IN_GLOBAL(c * 8 + 8 <= K, err)) {
+    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * K + static_cast<size_t>(c) * 8) = q;
+    const size_t so = fp8_sf_offset(row, c >> 4, sfb);
+    if ((c & 15) == 0 && SVDQ_IN_GLOBAL(so < nscale, err)) scales[so] = static_cast<uint8_t>(b);
+  }
+}
+
+// Zero scale bytes of the padding: thread t of n writes its share of the padding rows M .. Mpad-1
+// (a 4-byte word per row and block of groups) and of the padding groups of the rows below M.
+__device__ __forceinline__ void fp8_zero_padding(uint8_t* scales, int M, int K, int sfb, int64_t t, int64_t n) {
+  const int Mpad = (M + 127) / 128 * 128;
+  const int64_t words = static_cast<int64_t>(Mpad - M) * sfb;
+  for (int64_t i = t; i < words; i += n)
+    *reinterpret_cast<uint32_t*>(scales + fp8_sf_offset(M + static_cast<int>(i / sfb), 4 * static_cast<int>(i % sfb), sfb)) = 0u;
+}
+
+}  // namespace svdq

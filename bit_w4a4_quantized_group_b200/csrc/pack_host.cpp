@@ -5,7 +5,8 @@
 // saved together with the low-rank factors.  Formats follow §2.2 and §8 of
 // the same page: INT4 groups of 64 with a 16-bit scale (eq.(1), s = max|Z|/7),
 // NVFP4 groups of 16 with an FP8 (E4M3) scale; the 8-bit setting of §8 (appendix D)
-// quantizes each output channel of the weight with one scale (W8A8).  The rounding rules are the
+// quantizes each output channel of the weight with one scale (W8A8).  FP8 takes groups of 128
+// with a power-of-two scale each.  The rounding rules are the
 // ones stated in svdq.h; every conversion below is written from the format
 // definition (IEEE binary16, bfloat16, OCP E4M3 "fn", E2M1).
 #include <algorithm>
@@ -190,6 +191,30 @@ extern "C" svdq_status svdq_pack_weight(svdq_format fmt, int64_t N, int64_t K, i
           uint8_t c = 0;
           if (den > 0.0f) c = f32_to_e2m1_rn_sat(row[k] / den);
           codes[n * (K / 2) + k / 2] |= static_cast<uint8_t>((k & 1) ? (c << 4) : c);
+        }
+      }
+    }
+  } else if (fmt == SVDQ_FMT_FP8_G128) {
+    // X = 2^e, e the smallest exponent >= -127 with a <= 448 * 2^e, byte e + 127
+    uint8_t* sf = static_cast<uint8_t*>(w_scales);
+    const int64_t blocks = fp8_sf_blocks(K);
+    std::memset(sf, 0, static_cast<size_t>(Np) * static_cast<size_t>(4 * blocks));
+    for (int64_t n = 0; n < N; ++n) {
+      const float* row = R + n * K;
+      for (int64_t g = 0; g < K / 128; ++g) {
+        float a = 0.0f;
+        for (int j = 0; j < 128; ++j) a = std::fmax(a, std::fabs(row[g * 128 + j]));
+        int e = -127;
+        if (a > 0.0f) {
+          int ex = 0;
+          const float m = std::frexp(a, &ex);             // a = m 2^ex, m in [0.5, 1); 448 = 0.875 * 2^9
+          e = std::max(-127, ex - 9 + (m > 0.875f ? 1 : 0));
+        }
+        sf[blocked_sf_offset(n, g, blocks * 512, 128)] = static_cast<uint8_t>(e + 127);
+        for (int j = 0; j < 128; ++j) {
+          const float v = std::ldexp(row[g * 128 + j], -e);   // exact, or far below the smallest code
+          const uint8_t c = f32_to_e4m3_rn_sat(std::fabs(v));
+          codes[n * K + g * 128 + j] = static_cast<uint8_t>(c | (std::signbit(v) ? 0x80 : 0));
         }
       }
     }

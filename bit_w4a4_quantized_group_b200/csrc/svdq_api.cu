@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -129,6 +130,7 @@ size_t scale_bytes(svdq_format fmt, int64_t rows, int64_t K) {
   const int64_t rp = (rows + 127) / 128 * 128;
   if (fmt == SVDQ_FMT_INT4_G64) return static_cast<size_t>(rp * (K / 64) * 2);
   if (fmt == SVDQ_FMT_W8A8) return static_cast<size_t>(rp * 4);
+  if (fmt == SVDQ_FMT_FP8_G128) return static_cast<size_t>(rp * 4 * fp8_sf_blocks(K));
   return static_cast<size_t>(rp * (K / fp4_group(fmt)));
 }
 
@@ -205,6 +207,7 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
   t_last_launch_count = 0;
   svdq_status st = check_dims(fmt, M, 128, K, rank);
   if (st != SVDQ_OK) return st;
+  if (fmt == SVDQ_FMT_FP8_G128) return SVDQ_ERR_UNSUPPORTED;
   if (!X_bf16 || !a_codes || !a_scales) return SVDQ_ERR_INVALID_ARG;
   if (!aligned16(X_bf16) || !aligned16(a_codes) || !aligned16(a_scales)) return SVDQ_ERR_INVALID_ARG;
   if (lambda && !aligned16(lambda)) return SVDQ_ERR_INVALID_ARG;
@@ -257,6 +260,7 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
   t_last_launch_count = 0;
   svdq_status st = check_dims(fmt, M, N, K, rank);
   if (st != SVDQ_OK) return st;
+  if (fmt == SVDQ_FMT_FP8_G128) return SVDQ_ERR_UNSUPPORTED;
   if (!a_codes || !a_scales || !w_codes || !w_scales || !Y_bf16) return SVDQ_ERR_INVALID_ARG;
   if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
       !aligned16(Y_bf16))
@@ -362,6 +366,84 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
       return SVDQ_ERR_CUDA;
     e = launch_gemm_int4(ta, tb, tz, tl2, ty, tsa, tsb, p, sms, static_cast<cudaStream_t>(cuda_stream));
   }
+  if (e != cudaSuccess) return cuda_fail(e);
+  t_last_launch_count = 1;
+  return SVDQ_OK;
+}
+
+namespace {
+// A row-strided bf16 matrix argument: present, 16-byte aligned rows at least K elements apart.
+bool good_rows(const void* p, int64_t ld, int64_t K) {
+  return p && aligned16(p) && ld >= K && ld % 8 == 0 && ld <= (int64_t(1) << 40);
+}
+}  // namespace
+
+extern "C" svdq_status svdq_rmsnorm_quantize_act(svdq_format fmt, int64_t M, int64_t K, const void* X_bf16,
+                                                 int64_t ldx, const void* residual_bf16, int64_t ldr,
+                                                 const float* gamma, float eps, void* H_bf16, int64_t ldh,
+                                                 void* a_codes, void* a_scales, void* cuda_stream) {
+  t_last_launch_count = 0;
+  svdq_status st = check_dims(fmt, M, 128, K, 0);
+  if (st != SVDQ_OK) return st;
+  if (!good_rows(X_bf16, ldx, K) || (residual_bf16 && !good_rows(residual_bf16, ldr, K)))
+    return SVDQ_ERR_INVALID_ARG;
+  if (H_bf16 && (!residual_bf16 || !good_rows(H_bf16, ldh, K))) return SVDQ_ERR_INVALID_ARG;
+  // in place means the same rows
+  if (H_bf16 && ((H_bf16 == X_bf16 && ldh != ldx) || (H_bf16 == residual_bf16 && ldh != ldr)))
+    return SVDQ_ERR_INVALID_ARG;
+  if (gamma && !aligned16(gamma)) return SVDQ_ERR_INVALID_ARG;
+  if (!std::isnormal(eps) || eps < 0.f) return SVDQ_ERR_INVALID_ARG;
+  if (!a_codes || !a_scales || !aligned16(a_codes) || !aligned16(a_scales)) return SVDQ_ERR_INVALID_ARG;
+  if (fmt != SVDQ_FMT_FP8_G128) return SVDQ_ERR_UNSUPPORTED;
+  NormParams p{};
+  p.M = static_cast<int>(M);
+  p.K = static_cast<int>(K);
+  p.sfb = static_cast<int>(fp8_sf_blocks(K));
+  p.X = static_cast<const __nv_bfloat16*>(X_bf16);
+  p.ldx = ldx;
+  p.R = static_cast<const __nv_bfloat16*>(residual_bf16);
+  p.ldr = ldr;
+  p.gamma = gamma;
+  p.eps = eps;
+  p.H = static_cast<__nv_bfloat16*>(H_bf16);
+  p.ldh = ldh;
+  p.codes = static_cast<uint8_t*>(a_codes);
+  p.scales = static_cast<uint8_t*>(a_scales);
+  p.err = device_error_word();
+  if (!p.err) return SVDQ_ERR_CUDA;
+  cudaError_t e = launch_rmsnorm_quant(p, static_cast<cudaStream_t>(cuda_stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  t_last_launch_count = 1;
+  return SVDQ_OK;
+}
+
+extern "C" svdq_status svdq_glu_quantize_act(svdq_format fmt, svdq_activation act, int64_t M, int64_t K,
+                                             const void* gate_bf16, int64_t ldg, const void* up_bf16, int64_t ldu,
+                                             const float* lambda, void* a_codes, void* a_scales,
+                                             void* cuda_stream) {
+  t_last_launch_count = 0;
+  svdq_status st = check_dims(fmt, M, 128, K, 0);
+  if (st != SVDQ_OK) return st;
+  if (act != SVDQ_ACT_SILU && act != SVDQ_ACT_GELU_TANH) return SVDQ_ERR_INVALID_ARG;
+  if (!good_rows(gate_bf16, ldg, K) || (up_bf16 && !good_rows(up_bf16, ldu, K))) return SVDQ_ERR_INVALID_ARG;
+  if (lambda && !aligned16(lambda)) return SVDQ_ERR_INVALID_ARG;
+  if (!a_codes || !a_scales || !aligned16(a_codes) || !aligned16(a_scales)) return SVDQ_ERR_INVALID_ARG;
+  if (fmt != SVDQ_FMT_FP8_G128) return SVDQ_ERR_UNSUPPORTED;
+  GluParams p{};
+  p.act = act;
+  p.M = static_cast<int>(M);
+  p.K = static_cast<int>(K);
+  p.sfb = static_cast<int>(fp8_sf_blocks(K));
+  p.gate = static_cast<const __nv_bfloat16*>(gate_bf16);
+  p.ldg = ldg;
+  p.up = static_cast<const __nv_bfloat16*>(up_bf16);
+  p.ldu = ldu;
+  p.lam = lambda;
+  p.codes = static_cast<uint8_t*>(a_codes);
+  p.scales = static_cast<uint8_t*>(a_scales);
+  p.err = device_error_word();
+  if (!p.err) return SVDQ_ERR_CUDA;
+  cudaError_t e = launch_glu_quant(p, static_cast<cudaStream_t>(cuda_stream));
   if (e != cudaSuccess) return cuda_fail(e);
   t_last_launch_count = 1;
   return SVDQ_OK;

@@ -13,6 +13,7 @@ constexpr int kFmtNvfp4 = 1;
 constexpr int kFmtInt4 = 2;
 constexpr int kFmtMxfp4 = 3;
 constexpr int kFmtW8a8 = 4;
+constexpr int kFmtFp8 = 5;
 
 // Codes recorded in the device error word when a bounded wait runs out.
 enum : int {
@@ -144,6 +145,36 @@ struct GemmParams {
   int y_align32;             // Y is 32-byte aligned (256-bit stores)
   int ksplit;                // INT4: CTAs of a cluster that split one tile's K steps (1: none)
 };
+
+// Row kernels with an FP8 output; sfb = ceil(K/512) scale blocks per 128 rows.
+struct NormParams {
+  int M, K, sfb;
+  const __nv_bfloat16* X;
+  int64_t ldx;
+  const __nv_bfloat16* R;    // nullable: the residual
+  int64_t ldr;
+  const float* gamma;        // nullable
+  float eps;
+  __nv_bfloat16* H;          // nullable: x + r
+  int64_t ldh;
+  uint8_t* codes;            // [M][K]
+  uint8_t* scales;           // blocked E8M0
+  int* err;
+};
+struct GluParams {
+  int act;                   // svdq_activation
+  int M, K, sfb;
+  const __nv_bfloat16* gate;
+  int64_t ldg;
+  const __nv_bfloat16* up;   // nullable
+  int64_t ldu;
+  const float* lam;          // nullable
+  uint8_t* codes;
+  uint8_t* scales;
+  int* err;
+};
+cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s);
+cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s);
 
 cudaError_t launch_prologue(int fmt, const CUtensorMap& tx, const CUtensorMap& tl1, const ProParams& p,
                             cudaStream_t s);

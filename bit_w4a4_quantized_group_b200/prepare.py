@@ -65,7 +65,8 @@ def qdq_weight(fmt: str, R_nk: torch.Tensor) -> torch.Tensor:
     NVFP4 g16: s = e4m3(fp32(fp32(a / 6) / g_w)) with g_w the power-of-two tensor scale,
     q = e2m1(fp32(R / fp32(s g_w))).  MXFP4 g32: X = 2^clip(floor(log2 a) - 2, -127, 127),
     q = e2m1(R / X).  W8A8: one scale per row, s = fp32(a / 127), q = clamp(rint(fp32(R / s)),
-    -127, 127).  Returns g s q in fp64.
+    -127, 127).  FP8 g128: X = 2^e, the smallest e >= -127 with a <= 448 X, q = e4m3(R / X).
+    Returns g s q in fp64.
     """
     R = R_nk.to(torch.float32)
     N, K = R.shape
@@ -106,6 +107,13 @@ def qdq_weight(fmt: str, R_nk: torch.Tensor) -> torch.Tensor:
         X = ((e + 1023) << 52).view(torch.float64)                       # 2^e, built exactly
         q = _e2m1_rn((Rg.to(torch.float64) / X[..., None]).to(torch.float32))
         return (q * X[..., None]).reshape(N, K)
+    if fmt == "fp8":
+        Rg = R.reshape(N, K // 128, 128)
+        m, ex = torch.frexp(Rg.abs().amax(2))                            # a = m 2^ex; 448 = 0.875 * 2^9
+        e = torch.where(m > 0, (ex - 9 + (m > 0.875)).clamp(min=-127), -127).to(torch.int64)
+        X = ((e + 1023) << 52).view(torch.float64)                       # 2^e, built exactly
+        q = (Rg.to(torch.float64) / X[..., None]).to(torch.float32).to(torch.float8_e4m3fn)
+        return (q.to(torch.float64) * X[..., None]).reshape(N, K)
     raise ValueError(fmt)
 
 

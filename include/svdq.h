@@ -16,7 +16,11 @@
  *
  * Notation: M = tokens (b), K = input features (m), N = output features (n),
  * r = rank of the low-rank branch.  g = 16 (NVFP4), 32 (MXFP4) or 64 (INT4), G = K / g.
- * The W8A8 format (8-bit codes, one scale per row) runs through the same two calls.
+ * The W8A8 format (8-bit codes, one scale per row) and the FP8 format (E4M3 codes, one
+ * power-of-two scale per 128 elements) run through the same two calls.  Two more calls write
+ * FP8 activations where a transformer block makes them: svdq_rmsnorm_quantize_act (residual
+ * addition and RMS norm before a projection) and svdq_glu_quantize_act (the activation
+ * between the two layers of an MLP); their outputs feed the GEMM of a rank-0 layer.
  *
  * Conventions for every call
  *   - Ownership: the caller owns every buffer.  The library never allocates
@@ -54,11 +58,17 @@
  *                                        NVFP4, MXFP4: E2M1 code (bit 3 = sign);
  *                                        INT4: 4-bit two's complement in -7..7.
  *            W8A8: s8 [rows][K]          one byte per element, two's complement in -127..127.
+ *            FP8:  u8 [rows][K]          one E4M3 byte per element (bit 7 = sign).
  *   NVFP4 scales  u8 (E4M3), MXFP4 scales u8 (E8M0: the scale is 2^(byte - 127)), both in the
  *       "128x4 blocked" layout, rows padded to Rp = ceil(rows/128)*128:
  *       byte offset of (row, grp) = ((row/128)*(K/(4g)) + grp/4)*512
  *                                   + (row%32)*16 + ((row%128)/32)*4 + grp%4
  *       size = Rp * K / g bytes.  Padding rows hold 0.
+ *   FP8 scales    u8 (E8M0: the scale is 2^(byte - 127)), g = 128, in the same blocked layout
+ *       with the groups of a row padded to Gp = ceil(K/512)*4:
+ *       byte offset of (row, grp) = ((row/128)*(Gp/4) + grp/4)*512
+ *                                   + (row%32)*16 + ((row%128)/32)*4 + grp%4
+ *       size = Rp * Gp bytes.  Padding rows and padding groups hold 0.
  *   INT4 scales   fp16, group-major, rows padded to Rp = ceil(rows/128)*128:
  *       element offset of (row, grp) = grp*Rp + row;  size = Rp * (K/64) * 2 bytes.
  *   W8A8 scales   fp32 [Rp], one per row (per token for activations, per output
@@ -103,16 +113,29 @@ typedef enum {
    * the prologue, weights per output channel by the pack.  No tensor scale.
    * ("SVDQuant 阅读笔记" §8, appendix D: the 8-bit setting uses rank 16, per-token
    * dynamic activation quantization and per-channel weight quantization.) */
-  SVDQ_FMT_W8A8 = 4
+  SVDQ_FMT_W8A8 = 4,
+  /* E4M3 codes, groups of 128 along K (activations and weights alike), one power-of-two scale
+   * per group stored as its E8M0 byte: X = 2^e with the smallest e >= -127 for which
+   * a <= 448 * 2^e, a = max|x| of the group, so that no code saturates (448 is the largest
+   * E4M3 value); q = e4m3(x / X), round to nearest even.  A zero group gets byte 0.  A scale
+   * shared by a 128 x 128 block of a weight is the case in which 128 rows hold the same byte.
+   * No tensor scale. */
+  SVDQ_FMT_FP8_G128 = 5
 } svdq_format;
+
+/* Activations of svdq_glu_quantize_act. */
+typedef enum {
+  SVDQ_ACT_SILU = 1,       /* x / (1 + exp(-x)) */
+  SVDQ_ACT_GELU_TANH = 2   /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+} svdq_activation;
 
 /* Byte sizes of every buffer of one layer call (no allocation happens). */
 typedef struct {
   size_t x;          /* X      M*K*2                */
-  size_t a_codes;    /* M*K/2 (W8A8: M*K)           */
+  size_t a_codes;    /* M*K/2 (W8A8, FP8: M*K)      */
   size_t a_scales;   /* per the scale layout above  */
   size_t z;          /* M*r*2                       */
-  size_t w_codes;    /* N*K/2 (W8A8: N*K)           */
+  size_t w_codes;    /* N*K/2 (W8A8, FP8: N*K)      */
   size_t w_scales;   /* per the scale layout above  */
   size_t l1;         /* r*K*2                       */
   size_t l2;         /* N*r*2                       */
@@ -139,12 +162,13 @@ svdq_status svdq_buffer_sizes(svdq_format fmt, int64_t M, int64_t N, int64_t K, 
  *                       with a = max|x| over the group (a zero scale gives zero codes)
  *                       MXFP4: the rule of SVDQ_FMT_MXFP4_G32 (a zero group gets byte 0)
  *                       W8A8: the rule of SVDQ_FMT_W8A8, one scale per row of R
+ *                       FP8: the rule of SVDQ_FMT_FP8_G128
  *   *w_gscale           NVFP4: g_w = 2^ceil(log2(max|R| / (6*448))) (1 if R == 0);
- *                       INT4, MXFP4, W8A8: 1
+ *                       INT4, MXFP4, W8A8, FP8: 1
  *   L1_bf16             bf16 of L1 (round to nearest even)
  *   L2_bf16             bf16 of bf16(L2) / (act_gscale * g_w); must be exact
  * act_gscale is the activation tensor scale later given to the device calls
- * (a positive power of two; 1 for INT4, MXFP4 and W8A8).  Returns SVDQ_ERR_INVALID_ARG for
+ * (a positive power of two; 1 for every format but NVFP4).  Returns SVDQ_ERR_INVALID_ARG for
  * bad sizes / NULL pointers / a non power-of-two act_gscale, and
  * SVDQ_ERR_UNSUPPORTED if pre-dividing L2 would not be exact in bf16.
  */
@@ -157,7 +181,7 @@ svdq_status svdq_pack_weight(svdq_format fmt, int64_t N, int64_t K, int rank, fl
  * Device prologue ("算法 2" steps 1-3 of "SVDQuant 阅读笔记" §6.1): one read of X.
  *   X_hat = bf16(fp32(X) / lambda)            (IEEE fp32 divide, one bf16 rounding)
  *   a_codes, a_scales = group quantization of X_hat along K (rules of svdq_pack_weight,
- *                       with act_gscale in place of g_w; INT4, MXFP4 and W8A8 require
+ *                       with act_gscale in place of g_w; every format but NVFP4 requires
  *                       act_gscale == 1).  W8A8 quantizes each token row with its own
  *                       scale, so its prologue reads X twice: once for the row maxima
  *                       (and Z), once to write the codes (the second read is served
@@ -180,6 +204,9 @@ svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M, int64_t K
  * W8A8: Y = bf16( s_x[m] s_w[n] sum_k q_x q_w + Z L2^T + bias ), the 8-bit sum exact in
  * an s32 accumulator and the low-rank product in a second, fp32 accumulator, both on
  * the tensor cores and combined in the epilogue (act_gscale = w_gscale = 1, L2s = L2).
+ * FP8: Y = bf16( sum_G 2^(e_x + e_w) sum_{k in G} q_x q_w + Z L2^T + bias ), all in one fp32
+ * accumulator (act_gscale = w_gscale = 1, L2s = L2).  With few tokens the call is bound by
+ * reading the weights; a kernel whose tiles are narrow along M then splits K over the SMs.
  * Z and L2s may be NULL when rank == 0; bias may be NULL.
  * Stream order is kept: the GEMM is launched so that it may start its set-up while the
  * kernel before it on the stream (normally this library's prologue) finishes, but it reads
@@ -190,6 +217,44 @@ svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int64_t N, int
                                       const void* w_codes, const void* w_scales, float w_gscale,
                                       const void* Z_bf16, const void* L2_bf16,
                                       const void* bias_bf16, void* Y_bf16, void* cuda_stream);
+
+/*
+ * Device RMS norm with the residual's addition and an FP8 output (fmt = SVDQ_FMT_FP8_G128;
+ * other formats return SVDQ_ERR_UNSUPPORTED):
+ *   h = X                                  without a residual
+ *   h = bf16(fp32(X) + fp32(residual))     with one; written to H when H is not NULL
+ *   y = (h * rsqrt(mean_k(h^2) + eps)) * gamma      in fp32 (gamma NULL means 1)
+ *   a_codes, a_scales = quantization of y along K (rule of SVDQ_FMT_FP8_G128), from the fp32
+ *                       values: y is not rounded to bf16 first
+ * Rows of X, residual and H start ldx, ldr and ldh elements apart (each >= K and a multiple
+ * of 8; ldr and ldh are ignored where their pointer is NULL).  H may be X or residual itself
+ * (same pointer, same row stride); other overlaps of an output with another buffer are outside
+ * the contract.  H needs a residual.  gamma is fp32 [K]; the norm before a layer with smoothing
+ * factors takes gamma / lambda.  eps must be positive, normal and finite.  The sum of squares
+ * is kept in fp32: a row whose sum of squares exceeds its range is outside the contract.
+ * The outputs feed svdq_w4a4_gemm_lowrank_up with rank 0.
+ */
+svdq_status svdq_rmsnorm_quantize_act(svdq_format fmt, int64_t M, int64_t K,
+                                      const void* X_bf16, int64_t ldx,
+                                      const void* residual_bf16, int64_t ldr,
+                                      const float* gamma, float eps, void* H_bf16, int64_t ldh,
+                                      void* a_codes, void* a_scales, void* cuda_stream);
+
+/*
+ * Device activation with an FP8 output (fmt = SVDQ_FMT_FP8_G128; other formats return
+ * SVDQ_ERR_UNSUPPORTED), the input of an MLP's second layer:
+ *   y = act(gate) [* up] [/ lambda]        in fp32, from bf16 gate and up
+ *   a_codes, a_scales = quantization of y along K (rule of SVDQ_FMT_FP8_G128)
+ * gate and up are [M][K] with rows ldg and ldu elements apart (each >= K and a multiple of
+ * 8), so that both may be column slices of one wider GEMM output; up NULL means no gating
+ * (ldu is then ignored).  lambda is fp32 [K] as in svdq_quantize_act_lowrank_down, or NULL.
+ * act is evaluated to a few units in the last place of fp32.
+ * The outputs feed svdq_w4a4_gemm_lowrank_up with rank 0.
+ */
+svdq_status svdq_glu_quantize_act(svdq_format fmt, svdq_activation act, int64_t M, int64_t K,
+                                  const void* gate_bf16, int64_t ldg, const void* up_bf16, int64_t ldu,
+                                  const float* lambda, void* a_codes, void* a_scales,
+                                  void* cuda_stream);
 
 /* Human-readable name of a status. */
 const char* svdq_status_string(svdq_status s);

@@ -407,7 +407,27 @@ def quantize_int8_rowwise(x: np.ndarray):
             "scale_bits": s.view(np.uint32), "gscale": 1.0}
 
 
+def quantize_fp8_g128(x: np.ndarray):
+    """FP8 per 128-element group: E4M3 codes and one power-of-two (E8M0) scale.
+
+    X = 2^e with the smallest e >= -127 for which max|x| <= 448 * 2^e; q = e4m3(x / X).
+    """
+    x = np.asarray(x, dtype=np.float64)
+    rows, K = x.shape
+    xg = x.reshape(rows, K // 128, 128)
+    a = np.max(np.abs(xg), axis=2)
+    e = np.full(a.shape, -127, np.int64)
+    for cand in range(120, -128, -1):          # the last candidate that still holds a is the smallest
+        e = np.where(a <= np.ldexp(448.0, cand), cand, e)
+    X = np.ldexp(1.0, e)
+    codes, vals = e4m3_rn_satfinite(xg / X[..., None])
+    return {"codes": codes.reshape(rows, K), "q": vals.reshape(rows, K).astype(np.float64),
+            "scale": X, "scale_bits": (e + 127).astype(np.uint8), "gscale": 1.0}
+
+
 def quantize(fmt: str, x: np.ndarray, gscale: float = 1.0):
+    if fmt == "fp8":
+        return quantize_fp8_g128(x)
     if fmt == "w8a8":
         return quantize_int8_rowwise(x)
     if fmt == "int4":
@@ -423,7 +443,7 @@ def group_size(fmt: str, K: Optional[int] = None) -> int:
     """Elements per scale along K; W8A8 has one scale per row (the whole of K)."""
     if fmt == "w8a8":
         return K
-    return {"int4": 64, "nvfp4": 16, "mxfp4": 32}[fmt]
+    return {"int4": 64, "nvfp4": 16, "mxfp4": 32, "fp8": 128}[fmt]
 
 
 def dequantize(fmt: str, qd) -> np.ndarray:
