@@ -1,0 +1,405 @@
+// FP8 GEMM with the fused low-rank up projection (sm_100a, CTA pairs).
+//
+//   Y = bf16( sum_G 2^(e_x + e_w) sum_{k in G} q_x q_w + Z L2^T + bias ),   G = 128 elements of K.
+//
+// The scales are powers of two stored as E8M0 bytes, the scale type of kind::mxf8f6f4, so the
+// tensor cores apply them and one fp32 TMEM accumulator takes the whole of K: there is no
+// per-group promotion in the epilogue.  That kind wants one scale per row and 32 elements of K;
+// here the four MMAs (K = 32 each) of a 128-element group simply name the same byte, and a
+// 4-byte scale column, as tcgen05.cp brings it from a 128-row x 4-group block, serves 512
+// elements of K.
+//
+// Design:
+//   * clusters of two CTAs compute 256 x BN output tiles with cta_group::2 MMAs, each CTA
+//     holding 128 rows of A and BN/2 rows of B; persistent clusters take contiguous runs of the
+//     N-fastest tile numbering;
+//   * a ring slot holds one K step of 128 bytes per row of A and B and, at every fourth step, the
+//     scale blocks of the next four (512 bytes per 128 rows), all counted on one barrier of the
+//     leader CTA (each CTA loads into its own shared memory; no multicast loads);
+//   * the leader's MMA warp copies a slot's scale blocks into one of four TMEM scale buffers
+//     (two or three tcgen05.cp per four steps) and issues the MMAs behind them; the tensor pipe
+//     executes both in order;
+//   * ceil(r/64) further slots hold Z and L2 (bf16): kind::f16 MMAs add the branch onto the same
+//     accumulator;
+//   * eight epilogue warps per CTA drain TMEM into registers, hand the accumulator back, add the
+//     bias and store bf16 Y while the next tile's MMAs run.  BN < 256 leaves TMEM for two
+//     accumulators, so that the next tile's MMAs do not wait for the drain either.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "svdq_device.cuh"
+
+namespace svdq {
+namespace {
+
+constexpr int kBM = 256;                      // pair tile rows
+constexpr int kRows = 128;                    // A rows per CTA
+constexpr int kKTile = 128;                   // E4M3 elements (bytes) per row and pipeline step
+constexpr int kProdWarp = 0, kMmaWarp = 1, kEpiWarp0 = 4;   // epilogue warps start at a multiple of 4
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);      // 384: up to 168 registers per thread
+constexpr uint32_t kABytes = kRows * 128;
+constexpr uint32_t kSfBlk = 512;              // scales of 128 rows x 4 groups
+constexpr int kSfBufs = 4;
+constexpr uint32_t kSfBufCols = 12;           // A-scales 4 columns, B-scales up to 8
+constexpr uint32_t kTmemCols = 512;
+
+template <int BN>
+struct Cfg {
+  static constexpr int kBRows = BN / 2;                               // B rows per CTA
+  static constexpr uint32_t kBBytes = kBRows * 128;
+  static constexpr int kSfbBlks = BN > 128 ? 2 : 1;                   // 128-row scale blocks a tile's columns touch
+  static constexpr uint32_t kSfBytes = (1 + kSfbBlks) * kSfBlk;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + 2048;   // scales padded: operands stay 1024-aligned
+  static constexpr int kStages = BN == 256 ? 6 : BN == 192 ? 6 : BN == 128 ? 8 : 9;
+  static constexpr int kAccs = BN == 256 ? 1 : 2;                     // accumulators in TMEM
+  static constexpr uint32_t kTmemSf0 = kAccs * BN;
+  static constexpr int kColsPerWarp = BN / 2;                         // epilogue columns of a warp
+  static_assert(kTmemSf0 + kSfBufs * kSfBufCols <= kTmemCols, "TMEM");
+};
+
+// E4M3 x E4M3 with UE8M0 scales (bit 23); sf_id (bits 29-30 for A, 4-5 for B) selects the byte of
+// the TMEM scale columns.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n, uint32_t sf_id) {
+  return (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(m >> 4) << 24) | (sf_id << 29) |
+         (sf_id << 4);
+}
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
+  // bf16 x bf16 -> fp32, K-major A and B
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+template <int BN>
+struct SharedTail {
+  uint64_t full[Cfg<BN>::kStages];    // slot holds its step (TMA bytes of both CTAs)
+  uint64_t empty[Cfg<BN>::kStages];   // the MMAs and copies that read the slot have completed
+  uint64_t sf_free[kSfBufs];          // the MMAs that read the TMEM scale buffer have completed
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                    const __grid_constant__ CUtensorMap tmap_sfa, const __grid_constant__ CUtensorMap tmap_sfb,
+                    const __grid_constant__ CUtensorMap tmap_z, const __grid_constant__ CUtensorMap tmap_l2,
+                    GemmParams p) {
+  using C = Cfg<BN>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  SharedTail<BN>* sh = reinterpret_cast<SharedTail<BN>*>(smem + C::kStages * C::kStageBytes);
+  volatile int* abort_flag = &sh->abort_flag;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();      // 0 = leader of the pair
+  const int cluster = blockIdx.x >> 1;
+  const int nclusters = gridDim.x >> 1;
+  const int nk = p.K / kKTile;
+  const int nk_lr = (p.rank + 63) / 64;
+  const TileSeq tiles(p.num_tiles, p.tiles_n, cluster, nclusters);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(&sh->full[s], 1);
+      ptx::mbar_init(&sh->empty[s], 1);
+    }
+    for (int b = 0; b < kSfBufs; ++b) ptx::mbar_init(&sh->sf_free[b], 1);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&sh->acc_full[b], 1);
+      ptx::mbar_init(&sh->acc_empty[b], 2 * kEpiWarps);
+    }
+    sh->abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc_pair(&sh->tmem_base, kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  // the set-up above may overlap the end of the kernel that writes A and Z
+  ptx::griddep_wait();
+
+  if (warp == kProdWarp) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      ptx::prefetch_tmap(&tmap_a);
+      ptx::prefetch_tmap(&tmap_b);
+      ptx::prefetch_tmap(&tmap_sfa);
+      ptx::prefetch_tmap(&tmap_sfb);
+      if (nk_lr > 0) {
+        ptx::prefetch_tmap(&tmap_z);
+        ptx::prefetch_tmap(&tmap_l2);
+      }
+      const uint64_t keep = ptx::l2_evict_last_policy();   // A and B tiles are re-read by other clusters
+      int it = 0;
+      bool ok = true;
+      for (int j = 0; j < tiles.count && ok; ++j) {
+        const int m0 = tiles.mb(j) * kBM + static_cast<int>(rank) * kRows;     // this CTA's A rows
+        const int n0 = tiles.nb(j) * BN;
+        const int nb0 = n0 + static_cast<int>(rank) * C::kBRows;               // this CTA's B rows
+        for (int k = 0; k < nk + nk_lr; ++k, ++it) {
+          const int s = it % C::kStages;
+          const uint32_t ph = (it / C::kStages) & 1;
+          if (!wait_bounded(&sh->empty[s], ph ^ 1u, abort_flag, p.err, kErrSiteGemmEmpty)) { ok = false; break; }
+          const uint32_t full_leader = ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0);
+          const uint32_t st = ptx::smem_u32(smem + s * C::kStageBytes);
+          const uint32_t sf = st + kABytes + C::kBBytes;
+          const bool with_sf = k < nk && (k & 3) == 0;
+          if (rank == 0)
+            ptx::mbar_arrive_expect_tx(&sh->full[s], 2 * (kABytes + C::kBBytes + (with_sf ? C::kSfBytes : 0u)));
+          if (k < nk) {
+            if (with_sf) {
+              ptx::tma_load_3d_pair_hint(sf, &tmap_sfa, full_leader, 0, k >> 2, m0 >> 7, keep);
+              ptx::tma_load_3d_pair_hint(sf + kSfBlk, &tmap_sfb, full_leader, 0, k >> 2, n0 >> 7, keep);
+            }
+            ptx::tma_load_2d_pair_hint(st, &tmap_a, full_leader, k * kKTile, m0, keep);
+            ptx::tma_load_2d_pair_hint(st + kABytes, &tmap_b, full_leader, k * kKTile, nb0, keep);
+          } else {
+            ptx::tma_load_2d_pair(st, &tmap_z, full_leader, (k - nk) * 64, m0);
+            ptx::tma_load_2d_pair(st + kABytes, &tmap_l2, full_leader, (k - nk) * 64, nb0);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer (leader CTA only)
+    if (rank == 0) {
+      int it = 0, sfi = 0;
+      bool ok = true;
+      const uint32_t id16 = idesc_bf16(kBM, BN);
+      for (int j = 0; j < tiles.count && ok; ++j) {
+        const int a = C::kAccs == 2 ? (j & 1) : 0;
+        const uint32_t use = static_cast<uint32_t>(C::kAccs == 2 ? j >> 1 : j);
+        if (!wait_bounded(&sh->acc_empty[a], (use & 1u) ^ 1u, abort_flag, p.err, kErrSiteGemmAccEmpty)) break;
+        ptx::tc_fence_after();
+        const uint32_t acc = tmem + static_cast<uint32_t>(a * BN);
+        // a tile that starts inside a 128-row scale block (BN 64 and 192) skips the block's first columns
+        const uint32_t sfb_skip = static_cast<uint32_t>((tiles.nb(j) * BN) & 127) / 32;
+        uint32_t sfa = 0, sfb = 0;
+        for (int k = 0; k < nk + nk_lr; ++k, ++it) {
+          const int s = it % C::kStages;
+          const uint32_t ph = (it / C::kStages) & 1;
+          if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t st = ptx::smem_u32(smem + s * C::kStageBytes);
+          if (k < nk) {
+            const int b = sfi % kSfBufs;
+            if ((k & 3) == 0) {
+              if (!wait_bounded(&sh->sf_free[b], ((sfi / kSfBufs) & 1) ^ 1u, abort_flag, p.err, kErrSiteGemmSfFree)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+              sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
+              sfb = sfa + 4;
+              if (lane == 0) {
+                const uint32_t sf = st + kABytes + C::kBBytes;
+                ptx::tmem_cp_32x128b_warpx4_pair(sfa, ptx::sdesc_sf(sf));
+#pragma unroll
+                for (int q = 0; q < C::kSfbBlks; ++q)
+                  ptx::tmem_cp_32x128b_warpx4_pair(sfb + 4 * q, ptx::sdesc_sf(sf + kSfBlk * (1 + q)));
+              }
+            }
+            if (lane == 0) {
+              const uint32_t id = static_cast<uint32_t>(k & 3);
+              const uint32_t idesc = idesc_mxf8(kBM, BN, id);
+#pragma unroll
+              for (int q = 0; q < kKTile / 32; ++q)
+                ptx::umma_mxf8_pair(acc, ptx::sdesc_sw128(st + q * 32), ptx::sdesc_sw128(st + kABytes + q * 32), idesc,
+                                    sfa | (id << 30), (sfb + sfb_skip) | (id << 30), (k | q) != 0 ? 1u : 0u);
+            }
+            if ((k & 3) == 3 || k == nk - 1) {
+              if (lane == 0) ptx::tc_commit_pair_local(&sh->sf_free[b]);
+              ++sfi;
+            }
+          } else if (lane == 0) {
+            const int nmma = min(64, p.rank - (k - nk) * 64) / 16;
+            for (int q = 0; q < nmma; ++q)
+              ptx::umma_f16_pair(acc, ptx::sdesc_sw128(st + q * 32), ptx::sdesc_sw128(st + kABytes + q * 32), id16, 1u);
+          }
+          if (lane == 0) ptx::tc_commit_pair(&sh->empty[s], 0x3);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) ptx::tc_commit_pair(&sh->acc_full[a], 0x3);
+        __syncwarp();
+      }
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------ epilogue (8 warps, both CTAs)
+    const int q = warp & 3;                 // TMEM lane quarter this warp may access
+    const int h = (warp - kEpiWarp0) >> 2;  // column half of the tile
+    constexpr int NC = C::kColsPerWarp / 32;
+    for (int j = 0; j < tiles.count; ++j) {
+      const int a = C::kAccs == 2 ? (j & 1) : 0;
+      const uint32_t use = static_cast<uint32_t>(C::kAccs == 2 ? j >> 1 : j);
+      const int m0 = tiles.mb(j) * kBM + static_cast<int>(rank) * kRows;
+      const int col0 = tiles.nb(j) * BN + h * C::kColsPerWarp;
+      if (!wait_bounded(&sh->acc_full[a], use & 1u, abort_flag, p.err, kErrSiteGemmAccFull)) break;
+      ptx::tc_fence_after();
+      // the warp's columns into registers, then the accumulator goes back to the MMA warp at once
+      uint32_t v[NC][32];
+      const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * BN + h * C::kColsPerWarp;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) ptx::tmem_ld_32x32b_x32(base + c * 32, v[c]);
+      ptx::tmem_wait_ld();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_peer(ptx::mapa_shared(ptx::smem_u32(&sh->acc_empty[a]), 0));
+      const int row = m0 + q * 32 + lane;
+      if (row >= p.M) continue;
+      __nv_bfloat16* yrow = p.Y + static_cast<size_t>(row) * p.N + col0;
+#pragma unroll
+      for (int c16 = 0; c16 < 2 * NC; ++c16) {
+        const int cl = c16 * 16;
+        if (col0 + cl >= p.N) break;                       // the last tile may reach past N
+        const bool in_n = SVDQ_IN_GLOBAL(col0 + cl + 16 <= p.N, p.err);
+        float bv[16];
+        if (p.bias && in_n) {
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb) {
+            const uint4 braw = __ldg(reinterpret_cast<const uint4*>(p.bias + col0 + cl + 8 * hb));
+            const uint32_t bw[4] = {braw.x, braw.y, braw.z, braw.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              bv[8 * hb + 2 * e] = __uint_as_float(bw[e] << 16);
+              bv[8 * hb + 2 * e + 1] = __uint_as_float(bw[e] & 0xFFFF0000u);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) bv[e] = 0.f;
+        }
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __nv_bfloat162 hv = __floats2bfloat162_rn(__uint_as_float(v[cl / 32][cl % 32 + 2 * e]) + bv[2 * e],
+                                                          __uint_as_float(v[cl / 32][cl % 32 + 2 * e + 1]) + bv[2 * e + 1]);
+          o[e] = *reinterpret_cast<const uint32_t*>(&hv);
+        }
+        if (!in_n) {
+        } else if (p.y_align32) {
+          ptx::st_global_v8_na(yrow + cl, o);
+        } else {
+          *reinterpret_cast<uint4*>(yrow + cl) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(yrow + cl + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
+    }
+  }
+
+  // Both CTAs finished: every MMA has completed (each epilogue saw its last accumulator) and no
+  // remote arrive is still in flight.
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+template <int BN>
+size_t smem_bytes() {
+  return 1024 + Cfg<BN>::kStages * Cfg<BN>::kStageBytes + sizeof(SharedTail<BN>);
+}
+
+template <int BN>
+int max_active_clusters(size_t smem) {
+  static int cache[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, gemm_fp8_kernel<BN>, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev >= 0 && dev < 64) cache[dev] = n;
+  return n;
+}
+
+template <int BN>
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsfa, const CUtensorMap& tsfb,
+                   const CUtensorMap& tz, const CUtensorMap& tl2, const GemmParams& p, int num_sms, cudaStream_t s) {
+  const size_t smem = smem_bytes<BN>();
+  static_assert(1024 + Cfg<BN>::kStages * Cfg<BN>::kStageBytes + sizeof(SharedTail<BN>) <= 232448,
+                "shared memory of one CTA");
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(gemm_fp8_kernel<BN>), smem);
+  if (e != cudaSuccess) return e;
+  int clusters = max_active_clusters<BN>(smem);
+  if (clusters <= 0) clusters = num_sms / 2;
+  if (clusters > p.num_tiles) clusters = p.num_tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * clusters, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // may start under the kernel before
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<BN>, ta, tb, tsfa, tsfb, tz, tl2, p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int gemm_fp8_tile_n(int M, int N, int num_sms) {
+  // The tile width with the least time: waves of the persistent clusters times the width of a tile
+  // (a step's MMA time is proportional to it); wider tiles win ties, since they move fewer bytes.
+  const int64_t tm = (M + kBM - 1) / kBM;
+  const int widths[4] = {256, 192, 128, 64};
+  int best = 256;
+  int64_t cost = INT64_MAX;
+  for (int w : widths) {
+    const int64_t tiles = tm * ((N + w - 1) / w);
+    const int64_t slots = num_sms / 2;
+    const int64_t c = (tiles + slots - 1) / slots * w;
+    if (c < cost) {
+      cost = c;
+      best = w;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_gemm_fp8(int bn, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsfa,
+                            const CUtensorMap& tsfb, const CUtensorMap& tz, const CUtensorMap& tl2,
+                            const GemmParams& p, int num_sms, cudaStream_t s) {
+  switch (bn) {
+    case 256: return launch<256>(ta, tb, tsfa, tsfb, tz, tl2, p, num_sms, s);
+    case 192: return launch<192>(ta, tb, tsfa, tsfb, tz, tl2, p, num_sms, s);
+    case 128: return launch<128>(ta, tb, tsfa, tsfb, tz, tl2, p, num_sms, s);
+    case 64: return launch<64>(ta, tb, tsfa, tsfb, tz, tl2, p, num_sms, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace svdq

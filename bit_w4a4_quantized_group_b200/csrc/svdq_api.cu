@@ -79,6 +79,14 @@ bool make_tmap_sf(CUtensorMap* m, const void* base, int64_t rows_pad, int64_t K,
                       kblocks * 512, 64, static_cast<uint32_t>(2 * 256 / (4 * g)), blocks);
 }
 
+// The FP8 scale layout seen as [rows/128][ceil(K/512)][64 x 8-byte words]: one box = `blocks` row
+// blocks x the scale block of 512 columns.
+bool make_tmap_sf8(CUtensorMap* m, const void* base, int64_t rows_pad, int64_t K, uint32_t blocks) {
+  const uint64_t kblocks = static_cast<uint64_t>(fp8_sf_blocks(K));
+  return make_tmap_3d(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT64, 64, kblocks, static_cast<uint64_t>(rows_pad / 128), 512,
+                      kblocks * 512, 64, 1, blocks);
+}
+
 }  // namespace
 
 cudaError_t set_smem_limit_once(const void* kernel, size_t smem) {
@@ -207,7 +215,6 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
   t_last_launch_count = 0;
   svdq_status st = check_dims(fmt, M, 128, K, rank);
   if (st != SVDQ_OK) return st;
-  if (fmt == SVDQ_FMT_FP8_G128) return SVDQ_ERR_UNSUPPORTED;
   if (!X_bf16 || !a_codes || !a_scales) return SVDQ_ERR_INVALID_ARG;
   if (!aligned16(X_bf16) || !aligned16(a_codes) || !aligned16(a_scales)) return SVDQ_ERR_INVALID_ARG;
   if (lambda && !aligned16(lambda)) return SVDQ_ERR_INVALID_ARG;
@@ -244,6 +251,7 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
   const int kf = fmt == SVDQ_FMT_NVFP4_G16   ? kFmtNvfp4
                  : fmt == SVDQ_FMT_MXFP4_G32 ? kFmtMxfp4
                  : fmt == SVDQ_FMT_W8A8      ? kFmtW8a8
+                 : fmt == SVDQ_FMT_FP8_G128  ? kFmtFp8
                                              : kFmtInt4;
   cudaError_t e = launch_prologue(kf, tx, tl1, p,
                                   static_cast<cudaStream_t>(cuda_stream));
@@ -260,7 +268,6 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
   t_last_launch_count = 0;
   svdq_status st = check_dims(fmt, M, N, K, rank);
   if (st != SVDQ_OK) return st;
-  if (fmt == SVDQ_FMT_FP8_G128) return SVDQ_ERR_UNSUPPORTED;
   if (!a_codes || !a_scales || !w_codes || !w_scales || !Y_bf16) return SVDQ_ERR_INVALID_ARG;
   if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
       !aligned16(Y_bf16))
@@ -323,6 +330,25 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
     }
     e = launch_gemm_fp4(fmt == SVDQ_FMT_MXFP4_G32, ta, tb, tsfa, tsfb, tz, tl2, p, sms,
                         static_cast<cudaStream_t>(cuda_stream));
+  } else if (fmt == SVDQ_FMT_FP8_G128) {
+    const int bn = gemm_fp8_tile_n(p.M, p.N, sms);
+    const uint32_t brows = static_cast<uint32_t>(bn / 2);       // B rows of one CTA of the pair
+    p.tiles_m = static_cast<int>((M + 255) / 256);
+    p.tiles_n = static_cast<int>((N + bn - 1) / bn);
+    p.num_tiles = p.tiles_m * p.tiles_n;
+    CUtensorMap ta, tb, tsfa, tsfb;
+    if (!make_tmap(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, M, 128, 128)) return SVDQ_ERR_CUDA;
+    if (!make_tmap(&tb, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, 128, brows)) return SVDQ_ERR_CUDA;
+    if (!make_tmap_sf8(&tsfa, a_scales, p.Mpad, K, 1)) return SVDQ_ERR_CUDA;
+    if (!make_tmap_sf8(&tsfb, w_scales, p.Npad, K, bn > 128 ? 2 : 1)) return SVDQ_ERR_CUDA;
+    if (rank > 0) {
+      if (!make_tmap(&tz, Z_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rank, M, 64, 128)) return SVDQ_ERR_CUDA;
+      if (!make_tmap(&tl2, L2_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rank, N, 64, brows)) return SVDQ_ERR_CUDA;
+    } else {
+      tz = ta;
+      tl2 = tb;
+    }
+    e = launch_gemm_fp8(bn, ta, tb, tsfa, tsfb, tz, tl2, p, sms, static_cast<cudaStream_t>(cuda_stream));
   } else if (fmt == SVDQ_FMT_W8A8) {
     p.tiles_m = static_cast<int>((M + 255) / 256);
     p.tiles_n = static_cast<int>((N + 255) / 256);

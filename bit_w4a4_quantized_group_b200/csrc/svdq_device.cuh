@@ -19,6 +19,7 @@ constexpr int kFmtFp8 = 5;
 enum : int {
   kErrSiteProEmpty = 1,
   kErrSiteProFull = 2,
+  kErrSiteProPair = 3,
   kErrSiteGemmEmpty = 11,
   kErrSiteGemmFull = 12,
   kErrSiteGemmAccEmpty = 13,
@@ -189,6 +190,11 @@ size_t gemm_int4_smem_bytes();
 cudaError_t launch_gemm_w8a8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tz,
                              const CUtensorMap& tl2, const CUtensorMap& ty, const GemmParams& p, int num_sms,
                              cudaStream_t s);
+// FP8 GEMM: CTA-pair tiles of 256 x bn, bn = gemm_fp8_tile_n(...) in {64, 128, 192, 256}.
+int gemm_fp8_tile_n(int M, int N, int num_sms);
+cudaError_t launch_gemm_fp8(int bn, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsfa,
+                            const CUtensorMap& tsfb, const CUtensorMap& tz, const CUtensorMap& tl2,
+                            const GemmParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_gemm_int4(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tz,
                              const CUtensorMap& tl2, const CUtensorMap& ty, const CUtensorMap& tsa,
                              const CUtensorMap& tsb, const GemmParams& p, int num_sms, cudaStream_t s);
