@@ -16,9 +16,8 @@
 //   * a ring slot holds one K step of 128 bytes per row of A and B and, at every fourth step, the
 //     scale blocks of the next four (512 bytes per 128 rows), all counted on one barrier of the
 //     leader CTA (each CTA loads into its own shared memory; no multicast loads);
-//   * the leader's MMA warp copies a slot's scale blocks into one of four TMEM scale buffers
-//     (two or three tcgen05.cp per four steps) and issues the MMAs behind them; the tensor pipe
-//     executes both in order;
+//   * a copy warp of the leader moves those blocks into one of four TMEM scale buffers (two or
+//     three tcgen05.cp per four steps) as they land, ahead of the MMA warp;
 //   * ceil(r/64) further slots hold Z and L2 (bf16): kind::f16 MMAs add the branch onto the same
 //     accumulator;
 //   * eight epilogue warps per CTA drain TMEM into registers, hand the accumulator back, add the
@@ -37,7 +36,7 @@ namespace {
 constexpr int kBM = 256;                      // pair tile rows
 constexpr int kRows = 128;                    // A rows per CTA
 constexpr int kKTile = 128;                   // E4M3 elements (bytes) per row and pipeline step
-constexpr int kProdWarp = 0, kMmaWarp = 1, kEpiWarp0 = 4;   // epilogue warps start at a multiple of 4
+constexpr int kProdWarp = 0, kMmaWarp = 1, kCopyWarp = 2, kEpiWarp0 = 4;   // epilogue warps start at a multiple of 4
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);      // 384: up to 168 registers per thread
 constexpr uint32_t kABytes = kRows * 128;
@@ -76,6 +75,7 @@ template <int BN>
 struct SharedTail {
   uint64_t full[Cfg<BN>::kStages];    // slot holds its step (TMA bytes of both CTAs)
   uint64_t empty[Cfg<BN>::kStages];   // the MMAs and copies that read the slot have completed
+  uint64_t sf_ready[kSfBufs];         // the TMEM scale buffer holds its four steps' scales
   uint64_t sf_free[kSfBufs];          // the MMAs that read the TMEM scale buffer have completed
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
@@ -109,7 +109,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&sh->full[s], 1);
       ptx::mbar_init(&sh->empty[s], 1);
     }
-    for (int b = 0; b < kSfBufs; ++b) ptx::mbar_init(&sh->sf_free[b], 1);
+    for (int b = 0; b < kSfBufs; ++b) {
+      ptx::mbar_init(&sh->sf_ready[b], 1);
+      ptx::mbar_init(&sh->sf_free[b], 1);
+    }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&sh->acc_full[b], 1);
       ptx::mbar_init(&sh->acc_empty[b], 2 * kEpiWarps);
@@ -173,10 +176,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer (leader CTA only)
+    // The whole warp runs the loop and the waits; one elected thread issues.
     if (rank == 0) {
-      int it = 0, sfi = 0;
+      int s = 0, b = 0;
+      uint32_t ph = 0, sfph = 0;           // parities of the ring slot and of the scale buffer
       bool ok = true;
       const uint32_t id16 = idesc_bf16(kBM, BN);
+      const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem));   // + bytes / 16 for any slot
       for (int j = 0; j < tiles.count && ok; ++j) {
         const int a = C::kAccs == 2 ? (j & 1) : 0;
         const uint32_t use = static_cast<uint32_t>(C::kAccs == 2 ? j >> 1 : j);
@@ -185,54 +191,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t acc = tmem + static_cast<uint32_t>(a * BN);
         // a tile that starts inside a 128-row scale block (BN 64 and 192) skips the block's first columns
         const uint32_t sfb_skip = static_cast<uint32_t>((tiles.nb(j) * BN) & 127) / 32;
-        uint32_t sfa = 0, sfb = 0;
-        for (int k = 0; k < nk + nk_lr; ++k, ++it) {
-          const int s = it % C::kStages;
-          const uint32_t ph = (it / C::kStages) & 1;
+        for (int k = 0; k < nk + nk_lr; ++k) {
           if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) { ok = false; break; }
+          const bool main_step = k < nk;
+          const uint32_t id = static_cast<uint32_t>(k & 3);     // byte of the scale columns
+          if (main_step && id == 0 &&
+              !wait_bounded(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) {
+            ok = false;
+            break;
+          }
           ptx::tc_fence_after();
-          const uint32_t st = ptx::smem_u32(smem + s * C::kStageBytes);
-          if (k < nk) {
-            const int b = sfi % kSfBufs;
-            if ((k & 3) == 0) {
-              if (!wait_bounded(&sh->sf_free[b], ((sfi / kSfBufs) & 1) ^ 1u, abort_flag, p.err, kErrSiteGemmSfFree)) {
-                ok = false;
-                break;
-              }
-              ptx::tc_fence_after();
-              sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
-              sfb = sfa + 4;
-              if (lane == 0) {
-                const uint32_t sf = st + kABytes + C::kBBytes;
-                ptx::tmem_cp_32x128b_warpx4_pair(sfa, ptx::sdesc_sf(sf));
-#pragma unroll
-                for (int q = 0; q < C::kSfbBlks; ++q)
-                  ptx::tmem_cp_32x128b_warpx4_pair(sfb + 4 * q, ptx::sdesc_sf(sf + kSfBlk * (1 + q)));
-              }
-            }
-            if (lane == 0) {
-              const uint32_t id = static_cast<uint32_t>(k & 3);
-              const uint32_t idesc = idesc_mxf8(kBM, BN, id);
+          const bool sf_done = main_step && (id == 3 || k == nk - 1);
+          const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
+          const uint32_t sfb = sfa + 4 + sfb_skip;
+          if (ptx::elect_one()) {
+            const uint64_t ad = desc0 + static_cast<uint64_t>(s) * (C::kStageBytes / 16);
+            const uint64_t bd = ad + kABytes / 16;
+            if (main_step) {
+              const uint32_t idesc = idesc_mxf8(kBM, BN, 0) | (id << 29) | (id << 4);
 #pragma unroll
               for (int q = 0; q < kKTile / 32; ++q)
-                ptx::umma_mxf8_pair(acc, ptx::sdesc_sw128(st + q * 32), ptx::sdesc_sw128(st + kABytes + q * 32), idesc,
-                                    sfa | (id << 30), (sfb + sfb_skip) | (id << 30), (k | q) != 0 ? 1u : 0u);
+                ptx::umma_mxf8_pair(acc, ad + 2 * q, bd + 2 * q, idesc, sfa | (id << 30), sfb | (id << 30),
+                                    (k | q) != 0 ? 1u : 0u);
+              if (sf_done) ptx::tc_commit_pair_local(&sh->sf_free[b]);
+            } else {
+              const int nmma = min(64, p.rank - (k - nk) * 64) / 16;
+              for (int q = 0; q < nmma; ++q) ptx::umma_f16_pair(acc, ad + 2 * q, bd + 2 * q, id16, 1u);
             }
-            if ((k & 3) == 3 || k == nk - 1) {
-              if (lane == 0) ptx::tc_commit_pair_local(&sh->sf_free[b]);
-              ++sfi;
-            }
-          } else if (lane == 0) {
-            const int nmma = min(64, p.rank - (k - nk) * 64) / 16;
-            for (int q = 0; q < nmma; ++q)
-              ptx::umma_f16_pair(acc, ptx::sdesc_sw128(st + q * 32), ptx::sdesc_sw128(st + kABytes + q * 32), id16, 1u);
+            ptx::tc_commit_pair(&sh->empty[s], 0x3);
+            if (k == nk + nk_lr - 1) ptx::tc_commit_pair(&sh->acc_full[a], 0x3);
           }
-          if (lane == 0) ptx::tc_commit_pair(&sh->empty[s], 0x3);
           __syncwarp();
+          if (sf_done && ++b == kSfBufs) { b = 0; sfph ^= 1u; }
+          if (++s == C::kStages) { s = 0; ph ^= 1u; }
         }
-        if (!ok) break;
-        if (lane == 0) ptx::tc_commit_pair(&sh->acc_full[a], 0x3);
-        __syncwarp();
+      }
+    }
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------------------ scale copier (leader CTA only)
+    // Every fourth step's slot brings the scale blocks of four steps; they go to the next TMEM
+    // buffer in both CTAs.  The MMA warp waits for the copies' completion, so a slot that it
+    // releases has also been copied.
+    if (rank == 0) {
+      int it = 0, b = 0;
+      uint32_t sfph = 1;
+      const uint64_t sfdesc0 = ptx::sdesc_sf(ptx::smem_u32(smem) + kABytes + C::kBBytes);
+      bool ok = true;
+      for (int j = 0; j < tiles.count && ok; ++j) {
+        for (int k = 0; k < nk; k += 4) {
+          const int s = (it + k) % C::kStages;
+          const uint32_t ph = ((it + k) / C::kStages) & 1;
+          if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull) ||
+              !wait_bounded(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint64_t sd = sfdesc0 + static_cast<uint64_t>(s) * (C::kStageBytes / 16);
+            const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
+            ptx::tmem_cp_32x128b_warpx4_pair(sfa, sd);
+#pragma unroll
+            for (int q = 0; q < C::kSfbBlks; ++q)
+              ptx::tmem_cp_32x128b_warpx4_pair(sfa + 4 + 4 * q, sd + kSfBlk / 16 * (1 + q));
+            ptx::tc_commit_pair_local(&sh->sf_ready[b]);
+          }
+          __syncwarp();
+          if (++b == kSfBufs) { b = 0; sfph ^= 1u; }
+        }
+        it += nk + nk_lr;
       }
     }
   } else if (warp >= kEpiWarp0) {
