@@ -147,8 +147,10 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream():
+    """Raw handle of torch's current stream on the current device.  Read without building a
+    torch.cuda.Stream object (3 us), which would cost as much as the launch of a small call."""
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(st: int, what: str):
@@ -199,40 +201,42 @@ def w4a4_gemm_lowrank_up_t(fmt, M, N, K, rank, a_codes, a_scales, act_gscale, w_
     _check(st, "svdq_w4a4_gemm_lowrank_up")
 
 
-def _rows(t):
-    """(pointer, row stride in elements) of a [M, K] tensor with contiguous rows; (None, 0) for None."""
+def _rows(t, shape, like, name):
+    """(pointer, row stride in elements) of a matrix of that shape with contiguous rows, of the
+    type and on the device of `like`; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.stride(1) != 1 and t.shape[1] > 1:
-        raise ValueError("the elements of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _same_matrix(ref, **others):
-    """Every given tensor has ref's shape, 2-byte elements like ref, and ref's device."""
-    for name, t in others.items():
-        if t is not None and (t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device):
-            raise ValueError(f"{name}: expected {tuple(ref.shape)} {ref.dtype} on {ref.device}, got "
-                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    if t is not like and (t.shape != shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name}: expected {tuple(shape)} {like.dtype} on {like.device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
 def rmsnorm_quantize_act_t(fmt, X, residual, gamma, eps, H, a_codes, a_scales, stream=None):
     """Residual addition + RMS norm + quantization on torch tensors: X, residual, H bf16 [M, K] (rows
     may be strided; residual and H may be None), gamma fp32 [K] or None."""
-    M, K = X.shape
-    _same_matrix(X, residual=residual, H=H)
-    (x, ldx), (r, ldr), (h, ldh) = _rows(X), _rows(residual), _rows(H)
-    st = svdq_rmsnorm_quantize_act(fmt, M, K, x, ldx, r, ldr, _ptr(gamma), eps, h, ldh, _ptr(a_codes),
-                                   _ptr(a_scales), _stream() if stream is None else stream)
-    _check(st, "svdq_rmsnorm_quantize_act")
+    shape = X.shape
+    x, ldx = _rows(X, shape, X, "X")
+    r, ldr = _rows(residual, shape, X, "residual")
+    h, ldh = _rows(H, shape, X, "H")
+    st = load().svdq_rmsnorm_quantize_act(_fmt(fmt), shape[0], shape[1], x, ldx, r, ldr, _ptr(gamma), eps, h, ldh,
+                                          a_codes.data_ptr(), a_scales.data_ptr(),
+                                          _stream() if stream is None else stream)
+    if st != SVDQ_OK:
+        raise SvdqError(st, "svdq_rmsnorm_quantize_act")
 
 
 def glu_quantize_act_t(fmt, act, gate, up, lam, a_codes, a_scales, stream=None):
     """act(gate) [* up] [/ lam] + quantization on torch tensors: act "silu" or "gelu" (tanh form), gate
     and up bf16 [M, K] (column slices of a wider tensor will do; up may be None), lam fp32 [K] or None."""
-    M, K = gate.shape
-    _same_matrix(gate, up=up)
-    (g, ldg), (u, ldu) = _rows(gate), _rows(up)
-    st = svdq_glu_quantize_act(fmt, act, M, K, g, ldg, u, ldu, _ptr(lam), _ptr(a_codes), _ptr(a_scales),
-                               _stream() if stream is None else stream)
-    _check(st, "svdq_glu_quantize_act")
+    shape = gate.shape
+    g, ldg = _rows(gate, shape, gate, "gate")
+    u, ldu = _rows(up, shape, gate, "up")
+    st = load().svdq_glu_quantize_act(_fmt(fmt), ACTIVATIONS[act], shape[0], shape[1], g, ldg, u, ldu, _ptr(lam),
+                                      a_codes.data_ptr(), a_scales.data_ptr(),
+                                      _stream() if stream is None else stream)
+    if st != SVDQ_OK:
+        raise SvdqError(st, "svdq_glu_quantize_act")

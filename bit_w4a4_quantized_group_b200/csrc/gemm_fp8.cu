@@ -52,7 +52,7 @@ struct Cfg {
   static constexpr int kSfbBlks = BN > 128 ? 2 : 1;                   // 128-row scale blocks a tile's columns touch
   static constexpr uint32_t kSfBytes = (1 + kSfbBlks) * kSfBlk;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + 2048;   // scales padded: operands stay 1024-aligned
-  static constexpr int kStages = BN == 256 ? 6 : BN == 192 ? 6 : BN == 128 ? 8 : 9;
+  static constexpr int kStages = BN >= 192 ? 6 : 8;                   // released two at a time
   static constexpr int kAccs = BN == 256 ? 1 : 2;                     // accumulators in TMEM
   static constexpr uint32_t kTmemSf0 = kAccs * BN;
   static constexpr int kColsPerWarp = BN / 2;                         // epilogue columns of a warp
@@ -74,7 +74,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
 template <int BN>
 struct SharedTail {
   uint64_t full[Cfg<BN>::kStages];    // slot holds its step (TMA bytes of both CTAs)
-  uint64_t empty[Cfg<BN>::kStages];   // the MMAs and copies that read the slot have completed
+  uint64_t empty[Cfg<BN>::kStages / 2];   // the MMAs that read slots 2i and 2i + 1 have completed
   uint64_t sf_ready[kSfBufs];         // the TMEM scale buffer holds its four steps' scales
   uint64_t sf_free[kSfBufs];          // the MMAs that read the TMEM scale buffer have completed
   uint64_t acc_full[2];
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(&sh->full[s], 1);
-      ptx::mbar_init(&sh->empty[s], 1);
+      if ((s & 1) == 0) ptx::mbar_init(&sh->empty[s >> 1], 1);
     }
     for (int b = 0; b < kSfBufs; ++b) {
       ptx::mbar_init(&sh->sf_ready[b], 1);
@@ -152,7 +152,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < nk + nk_lr; ++k, ++it) {
           const int s = it % C::kStages;
           const uint32_t ph = (it / C::kStages) & 1;
-          if (!wait_bounded(&sh->empty[s], ph ^ 1u, abort_flag, p.err, kErrSiteGemmEmpty)) { ok = false; break; }
+          if ((s & 1) == 0 && !wait_bounded(&sh->empty[s >> 1], ph ^ 1u, abort_flag, p.err, kErrSiteGemmEmpty)) {
+            ok = false;
+            break;
+          }
           const uint32_t full_leader = ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0);
           const uint32_t st = ptx::smem_u32(smem + s * C::kStageBytes);
           const uint32_t sf = st + kABytes + C::kBBytes;
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int nmma = min(64, p.rank - (k - nk) * 64) / 16;
               for (int q = 0; q < nmma; ++q) ptx::umma_f16_pair(acc, ad + 2 * q, bd + 2 * q, id16, 1u);
             }
-            ptx::tc_commit_pair(&sh->empty[s], 0x3);
+            if (s & 1) ptx::tc_commit_pair(&sh->empty[s >> 1], 0x3);
             if (k == nk + nk_lr - 1) ptx::tc_commit_pair(&sh->acc_full[a], 0x3);
           }
           __syncwarp();
@@ -399,8 +402,9 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorM
 }  // namespace
 
 int gemm_fp8_tile_n(int M, int N, int num_sms) {
-  // The tile width with the least time: waves of the persistent clusters times the width of a tile
-  // (a step's MMA time is proportional to it); wider tiles win ties, since they move fewer bytes.
+  // The tile width with the least time: waves of the persistent clusters times the time of a K step,
+  // which fits 230 + width (in units of a column's time; measured at 4608 x 12288 x 3072, us a step:
+  // 0.52, 0.445, 0.385 and 0.313 for widths 256, 192, 128 and 64).
   const int64_t tm = (M + kBM - 1) / kBM;
   const int widths[4] = {256, 192, 128, 64};
   int best = 256;
@@ -408,7 +412,7 @@ int gemm_fp8_tile_n(int M, int N, int num_sms) {
   for (int w : widths) {
     const int64_t tiles = tm * ((N + w - 1) / w);
     const int64_t slots = num_sms / 2;
-    const int64_t c = (tiles + slots - 1) / slots * w;
+    const int64_t c = (tiles + slots - 1) / slots * (230 + w);
     if (c < cost) {
       cost = c;
       best = w;

@@ -5,7 +5,9 @@
 // Both activations have the form x * sigmoid(t) = x / (1 + exp(-t)): SiLU with t = x, the tanh
 // form of GELU with t = 2 sqrt(2/pi) (x + 0.044715 x^3), since 1 + tanh(u) = 2 / (1 + exp(-2u)).
 // This form has no cancellation for negative x, and its ends are right without a branch: exp
-// overflows to infinity and x / infinity is -0, or underflows to 0 and leaves x.
+// overflows to infinity, whose reciprocal is 0, or underflows to 0 and leaves x.  exp and the
+// reciprocal are the hardware's approximations (2 and 1 units in the last place); a divide by
+// lambda is a product with its reciprocal.  All of it is far inside the E4M3 step of 2^-4.
 //
 // What bounds it: memory (3 bytes per element, 5 with gating).  A thread holds 8 elements (16
 // bytes of each input) of kRows rows of the same columns, so that all its loads are in flight
@@ -25,11 +27,19 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kRows = 4;
 
+// 1 + exp(-t); the factors of t carry -log2(e), so that exp is one ex2.
 template <int ACT>
 __device__ __forceinline__ float act_denominator(float x) {
-  // 1 + exp(-t)
-  const float t = ACT == SVDQ_ACT_SILU ? x : x * fmaf(x * x, 2.f * 0.7978845608028654f * 0.044715f, 2.f * 0.7978845608028654f);
-  return 1.f + __expf(-t);
+  constexpr float kLog2e = 1.4426950408889634f, kC1 = 2.f * 0.7978845608028654f, kC3 = kC1 * 0.044715f;
+  const float t = ACT == SVDQ_ACT_SILU ? x * -kLog2e : x * fmaf(x * x, -kC3 * kLog2e, -kC1 * kLog2e);
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return 1.f + e;
+}
+__device__ __forceinline__ float rcp_approx_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 template <int ACT, bool GATED, bool LAM>
@@ -62,8 +72,9 @@ __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
   if (LAM) {
     const float4 l0 = on ? __ldg(reinterpret_cast<const float4*>(p.lam) + 2 * c) : make_float4(1.f, 1.f, 1.f, 1.f);
     const float4 l1 = on ? __ldg(reinterpret_cast<const float4*>(p.lam) + 2 * c + 1) : make_float4(1.f, 1.f, 1.f, 1.f);
-    lam[0] = l0.x; lam[1] = l0.y; lam[2] = l0.z; lam[3] = l0.w;
-    lam[4] = l1.x; lam[5] = l1.y; lam[6] = l1.z; lam[7] = l1.w;
+    // reciprocals, used for kRows rows
+    lam[0] = __frcp_rn(l0.x); lam[1] = __frcp_rn(l0.y); lam[2] = __frcp_rn(l0.z); lam[3] = __frcp_rn(l0.w);
+    lam[4] = __frcp_rn(l1.x); lam[5] = __frcp_rn(l1.y); lam[6] = __frcp_rn(l1.z); lam[7] = __frcp_rn(l1.w);
   }
   const int G = p.K >> 7, pad = 4 * p.sfb - G;
 #pragma unroll
@@ -77,10 +88,9 @@ __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float x = e & 1 ? bf16x2_hi(gx[e >> 1]) : bf16x2_lo(gx[e >> 1]);
-      float d = act_denominator<ACT>(x);
-      y[e] = x / d;
+      y[e] = x * rcp_approx_ftz(act_denominator<ACT>(x));
       if (GATED) y[e] *= e & 1 ? bf16x2_hi(ux[e >> 1]) : bf16x2_lo(ux[e >> 1]);
-      if (LAM) y[e] = y[e] / lam[e];
+      if (LAM) y[e] *= lam[e];
     }
     fp8_store_chunk(y, on, row, c, p.K, p.sfb, p.codes, p.scales, nscale, p.err);
     if (c < pad) p.scales[fp8_sf_offset(row, G + c, p.sfb)] = 0;      // padding groups (c < 3)

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -128,9 +129,19 @@ int device_sm_count() {
   return cache[dev];
 }
 
+// Address of the error word in the current device's copy of the library, looked up once per device.
 int* device_error_word() {
+  static std::atomic<int*> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  const bool cached = dev >= 0 && dev < 64;
+  if (cached) {
+    int* w = cache[dev].load(std::memory_order_relaxed);
+    if (w) return w;
+  }
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess) return nullptr;
+  if (cached) cache[dev].store(static_cast<int*>(p), std::memory_order_relaxed);
   return static_cast<int*>(p);
 }
 
