@@ -150,6 +150,15 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
         "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+// 32 lanes x 16 consecutive columns -> 16 registers per thread (thread i <-> lane i).
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // 16 lanes x 8 repeats of 256 bits (8 columns) -> 32 registers per thread.  Thread t of the
 // warp holds, for repeat i: r[4i], r[4i+1] = lane base + t/4, columns 8i + 2(t%4) + {0, 1};
 // r[4i+2], r[4i+3] = lane base + t/4 + 8, the same two columns.
@@ -266,6 +275,11 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4f32(uint32_t cluster_addr)
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(cluster_addr)
                : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_shared_cluster_v2f32(uint32_t cluster_addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr) : "memory");
   return v;
 }
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {

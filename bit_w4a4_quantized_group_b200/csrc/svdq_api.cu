@@ -342,24 +342,33 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
     e = launch_gemm_fp4(fmt == SVDQ_FMT_MXFP4_G32, ta, tb, tsfa, tsfb, tz, tl2, p, sms,
                         static_cast<cudaStream_t>(cuda_stream));
   } else if (fmt == SVDQ_FMT_FP8_G128) {
-    const int bn = gemm_fp8_tile_n(p.M, p.N, sms);
-    const uint32_t brows = static_cast<uint32_t>(bn / 2);       // B rows of one CTA of the pair
-    p.tiles_m = static_cast<int>((M + 255) / 256);
+    // operand tiles of `xrows` tokens and `wrows` weights per CTA; a scale box spans `wblocks` row blocks
+    const int small = gemm_fp8_small_tokens(p.M);
+    const int bn = small ? 128 : gemm_fp8_tile_n(p.M, p.N, sms);
+    const uint32_t xrows = small ? static_cast<uint32_t>(small) : 128u;
+    const uint32_t wrows = small ? 128u : static_cast<uint32_t>(bn / 2);
+    const uint32_t wblocks = !small && bn > 128 ? 2 : 1;
+    p.tiles_m = static_cast<int>(small ? (M + small - 1) / small : (M + 255) / 256);
     p.tiles_n = static_cast<int>((N + bn - 1) / bn);
     p.num_tiles = p.tiles_m * p.tiles_n;
     CUtensorMap ta, tb, tsfa, tsfb;
-    if (!make_tmap(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, M, 128, 128)) return SVDQ_ERR_CUDA;
-    if (!make_tmap(&tb, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, 128, brows)) return SVDQ_ERR_CUDA;
+    if (!make_tmap(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, M, 128, xrows)) return SVDQ_ERR_CUDA;
+    if (!make_tmap(&tb, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, 128, wrows)) return SVDQ_ERR_CUDA;
     if (!make_tmap_sf8(&tsfa, a_scales, p.Mpad, K, 1)) return SVDQ_ERR_CUDA;
-    if (!make_tmap_sf8(&tsfb, w_scales, p.Npad, K, bn > 128 ? 2 : 1)) return SVDQ_ERR_CUDA;
+    if (!make_tmap_sf8(&tsfb, w_scales, p.Npad, K, wblocks)) return SVDQ_ERR_CUDA;
     if (rank > 0) {
-      if (!make_tmap(&tz, Z_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rank, M, 64, 128)) return SVDQ_ERR_CUDA;
-      if (!make_tmap(&tl2, L2_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rank, N, 64, brows)) return SVDQ_ERR_CUDA;
+      if (!make_tmap(&tz, Z_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rank, M, 64, xrows)) return SVDQ_ERR_CUDA;
+      if (!make_tmap(&tl2, L2_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rank, N, 64, wrows)) return SVDQ_ERR_CUDA;
     } else {
       tz = ta;
       tl2 = tb;
     }
-    e = launch_gemm_fp8(bn, ta, tb, tsfa, tsfb, tz, tl2, p, sms, static_cast<cudaStream_t>(cuda_stream));
+    if (small) {
+      p.ksplit = gemm_fp8_small_split(p.num_tiles, p.K, sms);
+      e = launch_gemm_fp8_small(small, tb, ta, tsfb, tsfa, tl2, tz, p, static_cast<cudaStream_t>(cuda_stream));
+    } else {
+      e = launch_gemm_fp8(bn, ta, tb, tsfa, tsfb, tz, tl2, p, sms, static_cast<cudaStream_t>(cuda_stream));
+    }
   } else if (fmt == SVDQ_FMT_W8A8) {
     p.tiles_m = static_cast<int>((M + 255) / 256);
     p.tiles_n = static_cast<int>((N + 255) / 256);

@@ -144,7 +144,7 @@ struct GemmParams {
   int num_tiles, tiles_m, tiles_n;
   int op_pair;               // FP4: A and B tensor maps are 3-D and load two K steps at once
   int y_align32;             // Y is 32-byte aligned (256-bit stores)
-  int ksplit;                // INT4: CTAs of a cluster that split one tile's K steps (1: none)
+  int ksplit;                // INT4, FP8 with few tokens: CTAs of a cluster that split one tile's K steps (1: none)
 };
 
 // Row kernels with an FP8 output; sfb = ceil(K/512) scale blocks per 128 rows.
@@ -195,6 +195,13 @@ int gemm_fp8_tile_n(int M, int N, int num_sms);
 cudaError_t launch_gemm_fp8(int bn, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsfa,
                             const CUtensorMap& tsfb, const CUtensorMap& tz, const CUtensorMap& tl2,
                             const GemmParams& p, int num_sms, cudaStream_t s);
+// The same for few tokens: tiles of 128 weight rows x `tokens` (16, 32, 64 or 128; 0: use the kernel
+// above), K split over clusters of p.ksplit = gemm_fp8_small_split(...) CTAs.
+int gemm_fp8_small_tokens(int M);
+int gemm_fp8_small_split(int tiles, int K, int num_sms);
+cudaError_t launch_gemm_fp8_small(int tokens, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw,
+                                  const CUtensorMap& tsfx, const CUtensorMap& tl2, const CUtensorMap& tz,
+                                  const GemmParams& p, cudaStream_t s);
 cudaError_t launch_gemm_int4(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tz,
                              const CUtensorMap& tl2, const CUtensorMap& ty, const CUtensorMap& tsa,
                              const CUtensorMap& tsb, const GemmParams& p, int num_sms, cudaStream_t s);
