@@ -13,11 +13,11 @@
 //   * clusters of two CTAs compute 256 x BN output tiles with cta_group::2 MMAs, each CTA
 //     holding 128 rows of A and BN/2 rows of B; persistent clusters take contiguous runs of the
 //     N-fastest tile numbering;
-//   * a ring slot holds one K step of 128 bytes per row of A and B and, at every fourth step, the
-//     scale blocks of the next four (512 bytes per 128 rows), all counted on one barrier of the
+//   * a ring slot holds one K step of 128 bytes per row of A and B, counted on a barrier of the
 //     leader CTA (each CTA loads into its own shared memory; no multicast loads);
-//   * a copy warp of the leader moves those blocks into one of four TMEM scale buffers (two or
-//     three tcgen05.cp per four steps) as they land, ahead of the MMA warp;
+//   * the scale blocks (512 bytes per 128 rows and four steps) have a ring of their own: a copy
+//     warp of the leader moves them into the TMEM buffer of the same number (two or three
+//     tcgen05.cp per four steps) as they land, ahead of the MMA warp;
 //   * ceil(r/64) further slots hold Z and L2 (bf16): kind::f16 MMAs add the branch onto the same
 //     accumulator;
 //   * eight epilogue warps per CTA drain TMEM into registers, hand the accumulator back, add the
@@ -51,7 +51,7 @@ struct Cfg {
   static constexpr uint32_t kBBytes = kBRows * 128;
   static constexpr int kSfbBlks = BN > 128 ? 2 : 1;                   // 128-row scale blocks a tile's columns touch
   static constexpr uint32_t kSfBytes = (1 + kSfbBlks) * kSfBlk;
-  static constexpr uint32_t kStageBytes = kABytes + kBBytes + 2048;   // scales padded: operands stay 1024-aligned
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = BN >= 192 ? 6 : 8;                   // released two at a time
   static constexpr int kAccs = BN == 256 ? 1 : 2;                     // accumulators in TMEM
   static constexpr uint32_t kTmemSf0 = kAccs * BN;
@@ -75,8 +75,9 @@ template <int BN>
 struct SharedTail {
   uint64_t full[Cfg<BN>::kStages];    // slot holds its step (TMA bytes of both CTAs)
   uint64_t empty[Cfg<BN>::kStages / 2];   // the MMAs that read slots 2i and 2i + 1 have completed
-  uint64_t sf_ready[kSfBufs];         // the TMEM scale buffer holds its four steps' scales
-  uint64_t sf_free[kSfBufs];          // the MMAs that read the TMEM scale buffer have completed
+  uint64_t sf_full[kSfBufs];          // scale slot holds the blocks of four steps (TMA bytes of both CTAs)
+  uint64_t sf_ready[kSfBufs];         // ... and so does the TMEM buffer of the same number
+  uint64_t sf_free[kSfBufs];          // the MMAs that read the TMEM buffer have completed
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint32_t tmem_base;
@@ -92,7 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<BN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  SharedTail<BN>* sh = reinterpret_cast<SharedTail<BN>*>(smem + C::kStages * C::kStageBytes);
+  uint8_t* sf_smem = smem + C::kStages * C::kStageBytes;
+  SharedTail<BN>* sh = reinterpret_cast<SharedTail<BN>*>(sf_smem + kSfBufs * C::kSfBytes);
   volatile int* abort_flag = &sh->abort_flag;
 
   const int warp = threadIdx.x >> 5;
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((s & 1) == 0) ptx::mbar_init(&sh->empty[s >> 1], 1);
     }
     for (int b = 0; b < kSfBufs; ++b) {
+      ptx::mbar_init(&sh->sf_full[b], 1);
       ptx::mbar_init(&sh->sf_ready[b], 1);
       ptx::mbar_init(&sh->sf_free[b], 1);
     }
@@ -143,7 +146,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::prefetch_tmap(&tmap_l2);
       }
       const uint64_t keep = ptx::l2_evict_last_policy();   // A and B tiles are re-read by other clusters
-      int it = 0;
+      int it = 0, b = 0;
+      uint32_t sfph = 1;
       bool ok = true;
       for (int j = 0; j < tiles.count && ok; ++j) {
         const int m0 = tiles.mb(j) * kBM + static_cast<int>(rank) * kRows;     // this CTA's A rows
@@ -156,17 +160,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
+          if (k < nk && (k & 3) == 0) {
+            // the scale blocks of the next four steps
+            if (!wait_bounded(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree)) { ok = false; break; }
+            const uint32_t sf_leader = ptx::mapa_shared(ptx::smem_u32(&sh->sf_full[b]), 0);
+            const uint32_t sf = ptx::smem_u32(sf_smem + b * C::kSfBytes);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->sf_full[b], 2 * C::kSfBytes);
+            ptx::tma_load_3d_pair_hint(sf, &tmap_sfa, sf_leader, 0, k >> 2, m0 >> 7, keep);
+            ptx::tma_load_3d_pair_hint(sf + kSfBlk, &tmap_sfb, sf_leader, 0, k >> 2, n0 >> 7, keep);
+            if (++b == kSfBufs) { b = 0; sfph ^= 1u; }
+          }
           const uint32_t full_leader = ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0);
           const uint32_t st = ptx::smem_u32(smem + s * C::kStageBytes);
-          const uint32_t sf = st + kABytes + C::kBBytes;
-          const bool with_sf = k < nk && (k & 3) == 0;
-          if (rank == 0)
-            ptx::mbar_arrive_expect_tx(&sh->full[s], 2 * (kABytes + C::kBBytes + (with_sf ? C::kSfBytes : 0u)));
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->full[s], 2 * C::kStageBytes);
           if (k < nk) {
-            if (with_sf) {
-              ptx::tma_load_3d_pair_hint(sf, &tmap_sfa, full_leader, 0, k >> 2, m0 >> 7, keep);
-              ptx::tma_load_3d_pair_hint(sf + kSfBlk, &tmap_sfb, full_leader, 0, k >> 2, n0 >> 7, keep);
-            }
             ptx::tma_load_2d_pair_hint(st, &tmap_a, full_leader, k * kKTile, m0, keep);
             ptx::tma_load_2d_pair_hint(st + kABytes, &tmap_b, full_leader, k * kKTile, nb0, keep);
           } else {
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int q = 0; q < kKTile / 32; ++q)
                 ptx::umma_mxf8_pair(acc, ad + 2 * q, bd + 2 * q, idesc, sfa | (id << 30), sfb | (id << 30),
                                     (k | q) != 0 ? 1u : 0u);
-              if (sf_done) ptx::tc_commit_pair_local(&sh->sf_free[b]);
+              if (sf_done) ptx::tc_commit_pair(&sh->sf_free[b], 0x3);
             } else {
               const int nmma = min(64, p.rank - (k - nk) * 64) / 16;
               for (int q = 0; q < nmma; ++q) ptx::umma_f16_pair(acc, ad + 2 * q, bd + 2 * q, id16, 1u);
@@ -232,37 +239,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------ scale copier (leader CTA only)
-    // Every fourth step's slot brings the scale blocks of four steps; they go to the next TMEM
-    // buffer in both CTAs.  The MMA warp waits for the copies' completion, so a slot that it
-    // releases has also been copied.
+    // Scale slot b goes to TMEM buffer b in both CTAs.  The producers refill the slot only when the
+    // MMAs that read the buffer have completed, so slot and buffer are free together.
     if (rank == 0) {
-      int it = 0, b = 0;
-      uint32_t sfph = 1;
-      const uint64_t sfdesc0 = ptx::sdesc_sf(ptx::smem_u32(smem) + kABytes + C::kBBytes);
-      bool ok = true;
-      for (int j = 0; j < tiles.count && ok; ++j) {
-        for (int k = 0; k < nk; k += 4) {
-          const int s = (it + k) % C::kStages;
-          const uint32_t ph = ((it + k) / C::kStages) & 1;
-          if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull) ||
-              !wait_bounded(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          if (ptx::elect_one()) {
-            const uint64_t sd = sfdesc0 + static_cast<uint64_t>(s) * (C::kStageBytes / 16);
-            const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
-            ptx::tmem_cp_32x128b_warpx4_pair(sfa, sd);
+      int b = 0;
+      uint32_t sfph = 0;
+      const uint64_t sfdesc0 = ptx::sdesc_sf(ptx::smem_u32(sf_smem));
+      const int blocks = tiles.count * ((nk + 3) / 4);
+      for (int i = 0; i < blocks; ++i) {
+        if (!wait_bounded(&sh->sf_full[b], sfph, abort_flag, p.err, kErrSiteGemmFull)) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint64_t sd = sfdesc0 + static_cast<uint64_t>(b) * (C::kSfBytes / 16);
+          const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
+          ptx::tmem_cp_32x128b_warpx4_pair(sfa, sd);
 #pragma unroll
-            for (int q = 0; q < C::kSfbBlks; ++q)
-              ptx::tmem_cp_32x128b_warpx4_pair(sfa + 4 + 4 * q, sd + kSfBlk / 16 * (1 + q));
-            ptx::tc_commit_pair_local(&sh->sf_ready[b]);
-          }
-          __syncwarp();
-          if (++b == kSfBufs) { b = 0; sfph ^= 1u; }
+          for (int q = 0; q < C::kSfbBlks; ++q)
+            ptx::tmem_cp_32x128b_warpx4_pair(sfa + 4 + 4 * q, sd + kSfBlk / 16 * (1 + q));
+          ptx::tc_commit_pair_local(&sh->sf_ready[b]);
         }
-        it += nk + nk_lr;
+        __syncwarp();
+        if (++b == kSfBufs) { b = 0; sfph ^= 1u; }
       }
     }
   } else if (warp >= kEpiWarp0) {
@@ -340,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int BN>
 size_t smem_bytes() {
-  return 1024 + Cfg<BN>::kStages * Cfg<BN>::kStageBytes + sizeof(SharedTail<BN>);
+  return 1024 + Cfg<BN>::kStages * Cfg<BN>::kStageBytes + kSfBufs * Cfg<BN>::kSfBytes + sizeof(SharedTail<BN>);
 }
 
 template <int BN>
@@ -373,7 +370,7 @@ template <int BN>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsfa, const CUtensorMap& tsfb,
                    const CUtensorMap& tz, const CUtensorMap& tl2, const GemmParams& p, int num_sms, cudaStream_t s) {
   const size_t smem = smem_bytes<BN>();
-  static_assert(1024 + Cfg<BN>::kStages * Cfg<BN>::kStageBytes + sizeof(SharedTail<BN>) <= 232448,
+  static_assert(1024 + Cfg<BN>::kStages * Cfg<BN>::kStageBytes + kSfBufs * Cfg<BN>::kSfBytes + sizeof(SharedTail<BN>) <= 232448,
                 "shared memory of one CTA");
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(gemm_fp8_kernel<BN>), smem);
   if (e != cudaSuccess) return e;

@@ -5,14 +5,15 @@
 // empty and leave too few tiles for the SMs, so here the weights are the 128-row operand of the MMA
 // and the tokens its N side, T = 16, 32, 64 or 128 wide: D[n][m] = sum_k W[n][k] X[m][k].  The K
 // steps of a tile are split over a cluster of up to 8 CTAs, so that about two CTAs per SM stream
-// weights at once; with K = 4096 a CTA's whole share is in flight in its ring.  The CTAs' fp32
-// partial tiles are added through distributed shared memory, in CTA order (deterministic), and
-// the bias is added before the one rounding to bf16.
+// weights at once.  Each CTA sends its fp32 partial sums to the CTA that owns the token (tokens go
+// round the cluster) through distributed shared memory; after one cluster barrier the owner adds
+// them in CTA order (deterministic) and the bias before the one rounding to bf16.
 //
-// Scales: as in gemm_fp8.cu a 512-byte block serves four K steps; a CTA whose share starts inside
-// such a block loads that block with its first step.
+// Scales: as in gemm_fp8.cu a 512-byte block serves four K steps and has a ring of its own; a CTA
+// whose share starts inside such a block loads that block with its first step.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -28,16 +29,18 @@ constexpr int kThreads = 256;
 constexpr uint32_t kWBytes = kRowsW * 128;
 constexpr uint32_t kSfBlk = 512;
 constexpr int kSfBufs = 4;
+constexpr int kMaxSplit = 8;                  // portable cluster size
 
 template <int T>
 struct Cfg {
   static constexpr uint32_t kXBytes = T * 128;
-  static constexpr uint32_t kStageBytes = kWBytes + kXBytes + 2 * kSfBlk;
-  static constexpr int kStages = T <= 32 ? 5 : T == 64 ? 4 : 3;       // two CTAs per SM
+  static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
+  static constexpr int kStages = T == 16 ? 5 : T == 32 ? 4 : T == 64 ? 3 : 4;   // two CTAs per SM (T = 128: one)
+  // partial sums that the cluster's CTAs send here: [CTA][a CTA's share of the tokens][128]
+  static constexpr uint32_t kRedBytes = (T + kMaxSplit - 1) * kRowsW * 4;
   static constexpr uint32_t kTmemSf0 = T;
   static constexpr uint32_t kTmemCols = T <= 32 ? 64 : T == 64 ? 128 : 256;
   static_assert(T + kSfBufs * 8 <= kTmemCols, "TMEM");
-  static_assert(T * kRowsW * 4 <= kStages * kStageBytes, "the partial tile reuses the ring");
 };
 
 __host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n) {      // E4M3 x E4M3, UE8M0 scales
@@ -52,8 +55,9 @@ template <int T>
 struct SharedTail {
   uint64_t full[Cfg<T>::kStages];
   uint64_t empty[Cfg<T>::kStages];
-  uint64_t sf_ready[kSfBufs];
-  uint64_t sf_free[kSfBufs];
+  uint64_t sf_full[kSfBufs];     // scale slot holds the weights' and the tokens' block
+  uint64_t sf_ready[kSfBufs];    // ... and so does the TMEM buffer of the same number
+  uint64_t sf_free[kSfBufs];     // the MMAs that read the TMEM buffer have completed
   uint64_t acc_full;
   uint32_t tmem_base;
   int abort_flag;
@@ -68,7 +72,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   using C = Cfg<T>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  SharedTail<T>* sh = reinterpret_cast<SharedTail<T>*>(smem + C::kStages * C::kStageBytes);
+  uint8_t* sf_smem = smem + C::kStages * C::kStageBytes;
+  float* red = reinterpret_cast<float*>(sf_smem + kSfBufs * 2 * kSfBlk);
+  SharedTail<T>* sh = reinterpret_cast<SharedTail<T>*>(sf_smem + kSfBufs * 2 * kSfBlk + C::kRedBytes);
   volatile int* abort_flag = &sh->abort_flag;
 
   const int warp = threadIdx.x >> 5;
@@ -83,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int nk = static_cast<int>(static_cast<int64_t>(nk_all) * (split + 1) / ks) - kb;   // >= 1: ks <= nk_all
   const int nk_lr = split == ks - 1 ? (p.rank + 63) / 64 : 0; // the last CTA also takes the branch
   const int ntok = min(T, p.M - m0);
+  const int share = (T + ks - 1) / ks;                        // most tokens of the tile that one CTA adds up
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -90,6 +97,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_init(&sh->empty[s], 1);
     }
     for (int b = 0; b < kSfBufs; ++b) {
+      ptx::mbar_init(&sh->sf_full[b], 1);
       ptx::mbar_init(&sh->sf_ready[b], 1);
       ptx::mbar_init(&sh->sf_free[b], 1);
     }
@@ -104,33 +112,39 @@ __global__ void __launch_bounds__(kThreads, 2)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  if (ks > 1) ptx::cluster_arrive();      // waited for before anything is sent: every CTA has started
   const uint32_t tmem = sh->tmem_base;
   ptx::griddep_launch_dependents();
   // the set-up above may overlap the end of the kernel that writes X and Z
   ptx::griddep_wait();
 
-  // step k of this CTA (k < nk: the weights' K step kb + k) brings the scale blocks of the steps
-  // up to the next multiple of four
-  auto brings_scales = [&](int k) { return k < nk && (k == 0 || ((kb + k) & 3) == 0); };
+  // step k < nk of this CTA is the weights' K step kb + k; its first step, and each one that is a
+  // multiple of four, starts a scale block
+  auto starts_block = [&](int k) { return k < nk && (k == 0 || ((kb + k) & 3) == 0); };
 
   if (warp == kProdWarp) {
     if (lane == 0) {
       ptx::prefetch_tmap(&tmap_w);
       ptx::prefetch_tmap(&tmap_x);
+      int b = 0;
+      uint32_t sfph = 1;
       for (int k = 0; k < nk + nk_lr; ++k) {
         const int s = k % C::kStages;
         const uint32_t ph = (k / C::kStages) & 1;
         if (!wait_bounded(&sh->empty[s], ph ^ 1u, abort_flag, p.err, kErrSiteGemmEmpty)) break;
+        if (starts_block(k)) {
+          if (!wait_bounded(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree)) break;
+          uint8_t* sf = sf_smem + b * 2 * kSfBlk;
+          ptx::mbar_arrive_expect_tx(&sh->sf_full[b], 2 * kSfBlk);
+          ptx::tma_load_3d(sf, &tmap_sfw, &sh->sf_full[b], 0, (kb + k) >> 2, n0 >> 7);
+          ptx::tma_load_3d(sf + kSfBlk, &tmap_sfx, &sh->sf_full[b], 0, (kb + k) >> 2, m0 >> 7);
+          if (++b == kSfBufs) { b = 0; sfph ^= 1u; }
+        }
         uint8_t* st = smem + s * C::kStageBytes;
-        const bool sf = brings_scales(k);
-        ptx::mbar_arrive_expect_tx(&sh->full[s], kWBytes + C::kXBytes + (sf ? 2 * kSfBlk : 0u));
+        ptx::mbar_arrive_expect_tx(&sh->full[s], C::kStageBytes);
         if (k < nk) {
           ptx::tma_load_2d(st, &tmap_w, &sh->full[s], (kb + k) * kKTile, n0);
           ptx::tma_load_2d(st + kWBytes, &tmap_x, &sh->full[s], (kb + k) * kKTile, m0);
-          if (sf) {
-            ptx::tma_load_3d(st + kWBytes + C::kXBytes, &tmap_sfw, &sh->full[s], 0, (kb + k) >> 2, n0 >> 7);
-            ptx::tma_load_3d(st + kWBytes + C::kXBytes + kSfBlk, &tmap_sfx, &sh->full[s], 0, (kb + k) >> 2, m0 >> 7);
-          }
         } else {
           ptx::tma_load_2d(st, &tmap_l2, &sh->full[s], (k - nk) * 64, n0);
           ptx::tma_load_2d(st + kWBytes, &tmap_z, &sh->full[s], (k - nk) * 64, m0);
@@ -139,19 +153,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
   } else if (warp == kCopyWarp) {
+    // scale slot b -> TMEM buffer b; the producer refills the slot when the buffer is free
     int b = 0;
-    uint32_t sfph = 1;
-    const uint64_t sfdesc0 = ptx::sdesc_sf(ptx::smem_u32(smem) + kWBytes + C::kXBytes);
-    for (int k = 0; k < nk; ++k) {
-      if (!brings_scales(k)) continue;
-      const int s = k % C::kStages;
-      const uint32_t ph = (k / C::kStages) & 1;
-      if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull) ||
-          !wait_bounded(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree))
-        break;
+    uint32_t sfph = 0;
+    const uint64_t sfdesc0 = ptx::sdesc_sf(ptx::smem_u32(sf_smem));
+    const int blocks = ((kb + nk - 1) >> 2) - (kb >> 2) + 1;
+    for (int i = 0; i < blocks; ++i) {
+      if (!wait_bounded(&sh->sf_full[b], sfph, abort_flag, p.err, kErrSiteGemmFull)) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
-        const uint64_t sd = sfdesc0 + static_cast<uint64_t>(s) * (C::kStageBytes / 16);
+        const uint64_t sd = sfdesc0 + static_cast<uint64_t>(b) * (2 * kSfBlk / 16);
         const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * 8;
         ptx::tmem_cp_32x128b_warpx4(sfa, sd);
         ptx::tmem_cp_32x128b_warpx4(sfa + 4, sd + kSfBlk / 16);
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) break;
       const bool main_step = k < nk;
       const uint32_t id = static_cast<uint32_t>((kb + k) & 3);
-      if (brings_scales(k) && !wait_bounded(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) break;
+      if (starts_block(k) && !wait_bounded(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) break;
       ptx::tc_fence_after();
       const bool sf_done = main_step && (id == 3 || k == nk - 1);
       if (ptx::elect_one()) {
@@ -200,26 +211,29 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------------------ thread = weight row, column = token
     const int q = warp & 3;
     const int n = q * 32 + lane;
+    if (ks > 1) ptx::cluster_wait();
     if (wait_bounded(&sh->acc_full, 0u, abort_flag, p.err, kErrSiteGemmAccFull)) {
       ptx::tc_fence_after();
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
-      float* part = reinterpret_cast<float*>(smem);           // [token][128], the ring is drained
       const float bias = p.bias ? __bfloat162float(p.bias[n0 + n]) : 0.f;
+      const uint32_t red_mine = ptx::smem_u32(red) + static_cast<uint32_t>(split * share * kRowsW + n) * 4;
 #pragma unroll 1
       for (int c = 0; c < ntok; c += 16) {
         uint32_t v[16];
         ptx::tmem_ld_32x32b_x16(base + c, v);
         ptx::tmem_wait_ld();
-        if (ks > 1) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (SVDQ_IN_SMEM(smem_raw, part + (c + e) * kRowsW + n, 4, p.err))
-              part[(c + e) * kRowsW + n] = __uint_as_float(v[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (c + e < ntok && SVDQ_IN_GLOBAL(n0 + n < p.N, p.err))
-              p.Y[static_cast<size_t>(m0 + c + e) * p.N + n0 + n] = __float2bfloat16_rn(__uint_as_float(v[e]) + bias);
+        for (int e = 0; e < 16; ++e) {
+          if (c + e >= ntok) break;
+          if (ks > 1) {
+            // token c + e belongs to CTA (c + e) % ks, which keeps one slot per sender and token
+            const uint32_t slot = static_cast<uint32_t>((c + e) / ks * kRowsW) * 4;
+            if (SVDQ_IN_SMEM(smem_raw, red + (split * share + (c + e) / ks) * kRowsW + n, 4, p.err))
+              ptx::st_shared_cluster_f32(ptx::mapa_shared(red_mine + slot, static_cast<uint32_t>((c + e) % ks)),
+                                         __uint_as_float(v[e]));
+          } else if (SVDQ_IN_GLOBAL(n0 + n < p.N, p.err)) {
+            p.Y[static_cast<size_t>(m0 + c + e) * p.N + n0 + n] = __float2bfloat16_rn(__uint_as_float(v[e]) + bias);
+          }
         }
       }
       ptx::tc_fence_before();
@@ -227,11 +241,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 
   if (ks > 1) {
-    // Partial tiles of the cluster's CTAs, added in CTA order: CTA r takes the tokens r, r + ks, ...
-    // and a thread two neighbouring columns of one of them.
+    if (warp < kEpiWarp0) ptx::cluster_wait();       // the epilogue warps have waited
+    // CTA r adds the partial sums of the tokens r, r + ks, ... in the order of the sending CTAs; a
+    // thread takes two neighbouring columns of a token.  The barrier releases every CTA's sends, and
+    // nothing reaches into another CTA after it.
     ptx::cluster_sync();
     if (*abort_flag == 0) {
-      const uint32_t part = ptx::smem_u32(smem);
       const int col = 2 * (threadIdx.x & 63);
       float b0 = 0.f, b1 = 0.f;
       if (p.bias) {
@@ -239,25 +254,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         b0 = __uint_as_float(w << 16);
         b1 = __uint_as_float(w & 0xFFFF0000u);
       }
-      for (int c = split + ks * (threadIdx.x >> 6); c < ntok; c += ks * (kThreads / 64)) {
-        const uint32_t at = part + static_cast<uint32_t>(c * kRowsW + col) * 4;
-        float2 v[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < ks) v[r] = ptx::ld_shared_cluster_v2f32(ptx::mapa_shared(at, static_cast<uint32_t>(r)));
-        float s0 = v[0].x, s1 = v[0].y;
-#pragma unroll
-        for (int r = 1; r < 8; ++r)
-          if (r < ks) {
-            s0 += v[r].x;
-            s1 += v[r].y;
-          }
+      for (int i = threadIdx.x >> 6; split + ks * i < ntok; i += kThreads / 64) {
+        const float* src = red + i * kRowsW + col;
+        if (!SVDQ_IN_SMEM(smem_raw, src + (ks - 1) * share * kRowsW, 8, p.err)) continue;
+        float2 a = *reinterpret_cast<const float2*>(src);
+        for (int r = 1; r < ks; ++r) {
+          const float2 v = *reinterpret_cast<const float2*>(src + r * share * kRowsW);
+          a.x += v.x;
+          a.y += v.y;
+        }
         if (SVDQ_IN_GLOBAL(n0 + col + 2 <= p.N, p.err))
-          *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(m0 + c) * p.N + n0 + col) =
-              __floats2bfloat162_rn(s0 + b0, s1 + b1);
+          *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(m0 + split + ks * i) * p.N + n0 + col) =
+              __floats2bfloat162_rn(a.x + b0, a.y + b1);
       }
     }
-    ptx::cluster_sync();                                       // peers keep their partials until read
   } else {
     __syncthreads();
   }
@@ -268,26 +278,64 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <int T>
-cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw, const CUtensorMap& tsfx,
-                   const CUtensorMap& tl2, const CUtensorMap& tz, const GemmParams& p, cudaStream_t s) {
-  constexpr size_t smem = 1024 + Cfg<T>::kStages * Cfg<T>::kStageBytes + sizeof(SharedTail<T>);
-  static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
-  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(gemm_fp8_small_kernel<T>), smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.num_tiles) * static_cast<unsigned>(p.ksplit), 1, 1);
+constexpr size_t smem_bytes() {
+  return 1024 + Cfg<T>::kStages * Cfg<T>::kStageBytes + kSfBufs * 2 * kSfBlk + Cfg<T>::kRedBytes + sizeof(SharedTail<T>);
+}
+
+template <int T>
+void fill_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int clusters, int ks, cudaStream_t s) {
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters) * static_cast<unsigned>(ks), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = smem_bytes<T>();
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(p.ksplit);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // may start under the kernel before
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+}
+
+// Clusters of ks CTAs that the current device holds at once (0 on error), asked once per device.
+template <int T>
+int resident_clusters(int ks) {
+  static std::atomic<int> cache[64][kMaxSplit + 1];      // 0: not asked yet, else 1 + the figure
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const int known = cache[dev][ks].load(std::memory_order_relaxed);
+  if (known > 0) return known - 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  fill_config<T>(cfg, attr, 1, ks, nullptr);
+  cfg.numAttrs = 1;                                      // the cluster alone
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, gemm_fp8_small_kernel<T>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  cache[dev][ks].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+template <int T>
+cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw, const CUtensorMap& tsfx,
+                   const CUtensorMap& tl2, const CUtensorMap& tz, GemmParams p, cudaStream_t s) {
+  static_assert((T < 128 ? 2 : 1) * (smem_bytes<T>() + 1024) <= 228 * 1024, "shared memory of an SM");
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(gemm_fp8_small_kernel<T>), smem_bytes<T>());
+  if (e != cudaSuccess) return e;
+  // The widest split with every cluster resident at once: a second wave costs a whole pass.
+  const int nk = p.K / kKTile;
+  p.ksplit = 1;
+  for (int ks = nk < kMaxSplit ? nk : kMaxSplit; ks > 1; --ks)
+    if (resident_clusters<T>(ks) >= p.num_tiles) {
+      p.ksplit = ks;
+      break;
+    }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  fill_config<T>(cfg, attr, p.num_tiles, p.ksplit, s);
   e = cudaLaunchKernelEx(&cfg, gemm_fp8_small_kernel<T>, tw, tx, tsfw, tsfx, tl2, tz, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
@@ -298,14 +346,6 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorM
 int gemm_fp8_small_tokens(int M) {
   if (M > 128) return 0;
   return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-}
-
-int gemm_fp8_small_split(int tiles, int K, int num_sms) {
-  const int nk = K / kKTile;
-  int ks = 2 * num_sms / tiles;
-  if (ks > 8) ks = 8;
-  if (ks > nk) ks = nk;
-  return ks < 1 ? 1 : ks;
 }
 
 cudaError_t launch_gemm_fp8_small(int tokens, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw,

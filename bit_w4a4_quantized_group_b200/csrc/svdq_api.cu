@@ -363,12 +363,8 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
       tz = ta;
       tl2 = tb;
     }
-    if (small) {
-      p.ksplit = gemm_fp8_small_split(p.num_tiles, p.K, sms);
-      e = launch_gemm_fp8_small(small, tb, ta, tsfb, tsfa, tl2, tz, p, static_cast<cudaStream_t>(cuda_stream));
-    } else {
-      e = launch_gemm_fp8(bn, ta, tb, tsfa, tsfb, tz, tl2, p, sms, static_cast<cudaStream_t>(cuda_stream));
-    }
+    e = small ? launch_gemm_fp8_small(small, tb, ta, tsfb, tsfa, tl2, tz, p, static_cast<cudaStream_t>(cuda_stream))
+              : launch_gemm_fp8(bn, ta, tb, tsfa, tsfb, tz, tl2, p, sms, static_cast<cudaStream_t>(cuda_stream));
   } else if (fmt == SVDQ_FMT_W8A8) {
     p.tiles_m = static_cast<int>((M + 255) / 256);
     p.tiles_n = static_cast<int>((N + 255) / 256);

@@ -196,9 +196,8 @@ cudaError_t launch_gemm_fp8(int bn, const CUtensorMap& ta, const CUtensorMap& tb
                             const CUtensorMap& tsfb, const CUtensorMap& tz, const CUtensorMap& tl2,
                             const GemmParams& p, int num_sms, cudaStream_t s);
 // The same for few tokens: tiles of 128 weight rows x `tokens` (16, 32, 64 or 128; 0: use the kernel
-// above), K split over clusters of p.ksplit = gemm_fp8_small_split(...) CTAs.
+// above), K split over clusters (the launch picks p.ksplit).
 int gemm_fp8_small_tokens(int M);
-int gemm_fp8_small_split(int tiles, int K, int num_sms);
 cudaError_t launch_gemm_fp8_small(int tokens, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw,
                                   const CUtensorMap& tsfx, const CUtensorMap& tl2, const CUtensorMap& tz,
                                   const GemmParams& p, cudaStream_t s);
