@@ -5,9 +5,9 @@
 // empty and leave too few tiles for the SMs, so here the weights are the 128-row operand of the MMA
 // and the tokens its N side, T = 16, 32, 64 or 128 wide: D[n][m] = sum_k W[n][k] X[m][k].  The K
 // steps of a tile are split over a cluster of up to 8 CTAs, so that about two CTAs per SM stream
-// weights at once.  Each CTA sends its fp32 partial sums to the CTA that owns the token (tokens go
-// round the cluster) through distributed shared memory; after one cluster barrier the owner adds
-// them in CTA order (deterministic) and the bias before the one rounding to bf16.
+// weights at once.  Each CTA sends its fp32 partial sums to the CTA that owns the tokens, one bulk
+// copy through distributed shared memory per receiver; the owner adds them in CTA order
+// (deterministic) and the bias before the one rounding to bf16.
 //
 // Scales: as in gemm_fp8.cu a 512-byte block serves four K steps and has a ring of its own; a CTA
 // whose share starts inside such a block loads that block with its first step.
@@ -38,6 +38,7 @@ struct Cfg {
   static constexpr int kStages = T == 16 ? 5 : T == 32 ? 4 : T == 64 ? 3 : 4;   // two CTAs per SM (T = 128: one)
   // partial sums that the cluster's CTAs send here: [CTA][a CTA's share of the tokens][128]
   static constexpr uint32_t kRedBytes = (T + kMaxSplit - 1) * kRowsW * 4;
+  static_assert(T * kRowsW * 4 <= kStages * kStageBytes, "a CTA's own partial tile lies in its drained ring");
   static constexpr uint32_t kTmemSf0 = T;
   static constexpr uint32_t kTmemCols = T <= 32 ? 64 : T == 64 ? 128 : 256;
   static_assert(T + kSfBufs * 8 <= kTmemCols, "TMEM");
@@ -59,6 +60,7 @@ struct SharedTail {
   uint64_t sf_ready[kSfBufs];    // ... and so does the TMEM buffer of the same number
   uint64_t sf_free[kSfBufs];     // the MMAs that read the TMEM buffer have completed
   uint64_t acc_full;
+  uint64_t red_full;             // the other CTAs' partial sums of this CTA's tokens have arrived
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -89,7 +91,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int nk = static_cast<int>(static_cast<int64_t>(nk_all) * (split + 1) / ks) - kb;   // >= 1: ks <= nk_all
   const int nk_lr = split == ks - 1 ? (p.rank + 63) / 64 : 0; // the last CTA also takes the branch
   const int ntok = min(T, p.M - m0);
-  const int share = (T + ks - 1) / ks;                        // most tokens of the tile that one CTA adds up
+  // K split: CTA r adds up the tokens [r share, r share + own) of the tile
+  const int share = (ntok + ks - 1) / ks;
+  const int own = max(0, min(share, ntok - split * share));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -102,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::mbar_init(&sh->sf_free[b], 1);
     }
     ptx::mbar_init(&sh->acc_full, 1);
+    ptx::mbar_init(&sh->red_full, 1);
     sh->abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -112,7 +117,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (ks > 1) ptx::cluster_arrive();      // waited for before anything is sent: every CTA has started
+  if (ks > 1) {
+    if (threadIdx.x == 0)
+      ptx::mbar_arrive_expect_tx(&sh->red_full, static_cast<uint32_t>((ks - 1) * own * kRowsW * 4));
+    ptx::cluster_arrive();                // waited for before anything is sent: every CTA has started
+  }
   const uint32_t tmem = sh->tmem_base;
   ptx::griddep_launch_dependents();
   // the set-up above may overlap the end of the kernel that writes X and Z
@@ -216,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ptx::tc_fence_after();
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
       const float bias = p.bias ? __bfloat162float(p.bias[n0 + n]) : 0.f;
-      const uint32_t red_mine = ptx::smem_u32(red) + static_cast<uint32_t>(split * share * kRowsW + n) * 4;
+      float* part = reinterpret_cast<float*>(smem);           // [token][128], in the drained ring
 #pragma unroll 1
       for (int c = 0; c < ntok; c += 16) {
         uint32_t v[16];
@@ -226,11 +235,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int e = 0; e < 16; ++e) {
           if (c + e >= ntok) break;
           if (ks > 1) {
-            // token c + e belongs to CTA (c + e) % ks, which keeps one slot per sender and token
-            const uint32_t slot = static_cast<uint32_t>((c + e) / ks * kRowsW) * 4;
-            if (SVDQ_IN_SMEM(smem_raw, red + (split * share + (c + e) / ks) * kRowsW + n, 4, p.err))
-              ptx::st_shared_cluster_f32(ptx::mapa_shared(red_mine + slot, static_cast<uint32_t>((c + e) % ks)),
-                                         __uint_as_float(v[e]));
+            if (SVDQ_IN_SMEM(smem_raw, part + (c + e) * kRowsW + n, 4, p.err))
+              part[(c + e) * kRowsW + n] = __uint_as_float(v[e]);
           } else if (SVDQ_IN_GLOBAL(n0 + n < p.N, p.err)) {
             p.Y[static_cast<size_t>(m0 + c + e) * p.N + n0 + n] = __float2bfloat16_rn(__uint_as_float(v[e]) + bias);
           }
@@ -238,15 +244,32 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       ptx::tc_fence_before();
     }
+    if (ks > 1) {
+      // every other CTA gets its tokens' rows with one bulk copy
+      ptx::fence_proxy_async_smem();
+      named_barrier_sync(1, 128);
+      if (warp == kEpiWarp0 && lane < ks && lane != split && *abort_flag == 0) {
+        const int rows = min(share, ntok - lane * share);
+        if (rows > 0)
+          ptx::bulk_copy_to_cta(ptx::mapa_shared(ptx::smem_u32(red + split * share * kRowsW), static_cast<uint32_t>(lane)),
+                                reinterpret_cast<const float*>(smem) + lane * share * kRowsW,
+                                static_cast<uint32_t>(rows * kRowsW * 4),
+                                ptx::mapa_shared(ptx::smem_u32(&sh->red_full), static_cast<uint32_t>(lane)));
+      }
+      __syncwarp();
+    }
   }
 
   if (ks > 1) {
     if (warp < kEpiWarp0) ptx::cluster_wait();       // the epilogue warps have waited
-    // CTA r adds the partial sums of the tokens r, r + ks, ... in the order of the sending CTAs; a
-    // thread takes two neighbouring columns of a token.  The barrier releases every CTA's sends, and
-    // nothing reaches into another CTA after it.
-    ptx::cluster_sync();
-    if (*abort_flag == 0) {
+    // The partial sums are added in CTA order; a thread takes two neighbouring columns of a token.
+    // This CTA's own rows lie in its ring: written by its epilogue warps, which the barrier orders.
+    __syncthreads();
+    const bool ok = wait_bounded(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal);
+    // what the others sent has arrived; when all CTAs say so, every copy has left its source
+    __syncwarp();
+    ptx::cluster_arrive();
+    if (ok) {
       const int col = 2 * (threadIdx.x & 63);
       float b0 = 0.f, b1 = 0.f;
       if (p.bias) {
@@ -254,20 +277,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         b0 = __uint_as_float(w << 16);
         b1 = __uint_as_float(w & 0xFFFF0000u);
       }
-      for (int i = threadIdx.x >> 6; split + ks * i < ntok; i += kThreads / 64) {
-        const float* src = red + i * kRowsW + col;
-        if (!SVDQ_IN_SMEM(smem_raw, src + (ks - 1) * share * kRowsW, 8, p.err)) continue;
-        float2 a = *reinterpret_cast<const float2*>(src);
-        for (int r = 1; r < ks; ++r) {
-          const float2 v = *reinterpret_cast<const float2*>(src + r * share * kRowsW);
+      const float* mine = reinterpret_cast<const float*>(smem) + split * share * kRowsW + col;
+      for (int i = threadIdx.x >> 6; i < own; i += kThreads / 64) {
+        float2 a = make_float2(0.f, 0.f);
+        for (int r = 0; r < ks; ++r) {
+          const float* src = r == split ? mine + i * kRowsW : red + (r * share + i) * kRowsW + col;
+          if (!SVDQ_IN_SMEM(smem_raw, src, 8, p.err)) continue;
+          const float2 v = *reinterpret_cast<const float2*>(src);
           a.x += v.x;
           a.y += v.y;
         }
         if (SVDQ_IN_GLOBAL(n0 + col + 2 <= p.N, p.err))
-          *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(m0 + split + ks * i) * p.N + n0 + col) =
+          *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(m0 + split * share + i) * p.N + n0 + col) =
               __floats2bfloat162_rn(a.x + b0, a.y + b1);
       }
     }
+    __syncwarp();
+    ptx::cluster_wait();
   } else {
     __syncthreads();
   }
@@ -324,6 +350,8 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorM
                    const CUtensorMap& tl2, const CUtensorMap& tz, GemmParams p, cudaStream_t s) {
   static_assert((T < 128 ? 2 : 1) * (smem_bytes<T>() + 1024) <= 228 * 1024, "shared memory of an SM");
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(gemm_fp8_small_kernel<T>), smem_bytes<T>());
+  if (e != cudaSuccess) return e;
+  e = prefer_max_shared_once(reinterpret_cast<const void*>(gemm_fp8_small_kernel<T>));
   if (e != cudaSuccess) return e;
   // The widest split with every cluster resident at once: a second wave costs a whole pass.
   const int nk = p.K / kKTile;

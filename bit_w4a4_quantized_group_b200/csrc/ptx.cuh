@@ -277,8 +277,14 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4f32(uint32_t cluster_addr)
                : "memory");
   return v;
 }
-__device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+// Copy of `bytes` (a multiple of 16, 16-byte aligned at both ends) from this CTA's shared memory to a
+// shared::cluster address, counted on an mbarrier of the receiving CTA.
+__device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst_cluster, const void* src, uint32_t bytes,
+                                                 uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst_cluster),
+      "r"(smem_u32(src)), "r"(bytes), "r"(bar_cluster)
+      : "memory");
 }
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
   float v;

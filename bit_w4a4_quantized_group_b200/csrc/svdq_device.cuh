@@ -118,6 +118,9 @@ cudaError_t launch_selftest_bounded_wait(int* err, uint64_t limit_ns, cudaStream
 // per (kernel, device, size): the attribute belongs to the function in the device's context,
 // and setting it on every launch costs host time.
 cudaError_t set_smem_limit_once(const void* kernel, size_t smem);
+// Asks for the largest shared-memory share of the SM's on-chip memory, once per (kernel, device):
+// without it the driver may leave room for one CTA of a kernel of which two would fit.
+cudaError_t prefer_max_shared_once(const void* kernel);
 
 struct ProParams {
   int M, K, rank, Mpad, stages;
