@@ -4,8 +4,8 @@
 // With few tokens the work is reading the weights once.  A 256-row tile of tokens would be nearly
 // empty and leave too few tiles for the SMs, so here the weights are the 128-row operand of the MMA
 // and the tokens its N side, T = 16, 32, 64 or 128 wide: D[n][m] = sum_k W[n][k] X[m][k].  The K
-// steps of a tile are split over a cluster of up to 8 CTAs, so that about two CTAs per SM stream
-// weights at once.  Each CTA sends its fp32 partial sums to the CTA that owns the tokens, one bulk
+// steps of a tile are split over a cluster of up to 8 CTAs, so that most SMs stream weights at once
+// (one CTA per SM).  Each CTA sends its fp32 partial sums to the CTA that owns the tokens, one bulk
 // copy through distributed shared memory per receiver; the owner adds them in CTA order
 // (deterministic) and the bias before the one rounding to bf16.
 //
@@ -35,10 +35,11 @@ template <int T>
 struct Cfg {
   static constexpr uint32_t kXBytes = T * 128;
   static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
-  static constexpr int kStages = T == 16 ? 5 : T == 32 ? 4 : T == 64 ? 3 : 4;   // two CTAs per SM (T = 128: one)
+  static constexpr int kStages = T == 16 ? 10 : T == 32 ? 8 : T == 64 ? 7 : 4;       // at most
+  static constexpr int kMinStages = T == 16 ? 4 : T == 32 ? 4 : T == 64 ? 3 : 2;     // ... whose ring holds T * 512 bytes
   // partial sums that the cluster's CTAs send here: [CTA][a CTA's share of the tokens][128]
   static constexpr uint32_t kRedBytes = (T + kMaxSplit - 1) * kRowsW * 4;
-  static_assert(T * kRowsW * 4 <= kStages * kStageBytes, "a CTA's own partial tile lies in its drained ring");
+  static_assert(T * kRowsW * 4 <= kMinStages * kStageBytes, "a CTA's own partial tile lies in its drained ring");
   static constexpr uint32_t kTmemSf0 = T;
   static constexpr uint32_t kTmemCols = T <= 32 ? 64 : T == 64 ? 128 : 256;
   static_assert(T + kSfBufs * 8 <= kTmemCols, "TMEM");
@@ -66,7 +67,7 @@ struct SharedTail {
 };
 
 template <int T>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                           const __grid_constant__ CUtensorMap tmap_sfw, const __grid_constant__ CUtensorMap tmap_sfx,
                           const __grid_constant__ CUtensorMap tmap_l2, const __grid_constant__ CUtensorMap tmap_z,
@@ -74,7 +75,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   using C = Cfg<T>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sf_smem = smem + C::kStages * C::kStageBytes;
+  const int stages = p.stages;
+  uint8_t* sf_smem = smem + stages * C::kStageBytes;
   float* red = reinterpret_cast<float*>(sf_smem + kSfBufs * 2 * kSfBlk);
   SharedTail<T>* sh = reinterpret_cast<SharedTail<T>*>(sf_smem + kSfBufs * 2 * kSfBlk + C::kRedBytes);
   volatile int* abort_flag = &sh->abort_flag;
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int own = max(0, min(share, ntok - split * share));
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       ptx::mbar_init(&sh->full[s], 1);
       ptx::mbar_init(&sh->empty[s], 1);
     }
@@ -135,12 +137,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       ptx::prefetch_tmap(&tmap_w);
       ptx::prefetch_tmap(&tmap_x);
-      int b = 0;
-      uint32_t sfph = 1;
+      int s = 0, b = 0;
+      uint32_t ph = 1, sfph = 1;
       for (int k = 0; k < nk + nk_lr; ++k) {
-        const int s = k % C::kStages;
-        const uint32_t ph = (k / C::kStages) & 1;
-        if (!wait_bounded(&sh->empty[s], ph ^ 1u, abort_flag, p.err, kErrSiteGemmEmpty)) break;
+        if (!wait_bounded(&sh->empty[s], ph, abort_flag, p.err, kErrSiteGemmEmpty)) break;
         if (starts_block(k)) {
           if (!wait_bounded(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree)) break;
           uint8_t* sf = sf_smem + b * 2 * kSfBlk;
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           ptx::tma_load_2d(st, &tmap_l2, &sh->full[s], (k - nk) * 64, n0);
           ptx::tma_load_2d(st + kWBytes, &tmap_z, &sh->full[s], (k - nk) * 64, m0);
         }
+        if (++s == stages) { s = 0; ph ^= 1u; }
       }
     }
     __syncwarp();
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       __syncwarp();
       if (sf_done && ++b == kSfBufs) { b = 0; sfph ^= 1u; }
-      if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      if (++s == stages) { s = 0; ph ^= 1u; }
     }
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ thread = weight row, column = token
@@ -224,23 +225,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (wait_bounded(&sh->acc_full, 0u, abort_flag, p.err, kErrSiteGemmAccFull)) {
       ptx::tc_fence_after();
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
-      const float bias = p.bias ? __bfloat162float(p.bias[n0 + n]) : 0.f;
-      float* part = reinterpret_cast<float*>(smem);           // [token][128], in the drained ring
+      float* part = reinterpret_cast<float*>(smem) + n;       // [token][128], in the drained ring
+      constexpr int kCols = T < 32 ? T : 32;
 #pragma unroll 1
-      for (int c = 0; c < ntok; c += 16) {
-        uint32_t v[16];
-        ptx::tmem_ld_32x32b_x16(base + c, v);
-        ptx::tmem_wait_ld();
+      for (int c = 0; c < ntok; c += kCols) {
+        uint32_t v[kCols];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (c + e >= ntok) break;
-          if (ks > 1) {
-            if (SVDQ_IN_SMEM(smem_raw, part + (c + e) * kRowsW + n, 4, p.err))
-              part[(c + e) * kRowsW + n] = __uint_as_float(v[e]);
-          } else if (SVDQ_IN_GLOBAL(n0 + n < p.N, p.err)) {
-            p.Y[static_cast<size_t>(m0 + c + e) * p.N + n0 + n] = __float2bfloat16_rn(__uint_as_float(v[e]) + bias);
-          }
-        }
+        for (int h = 0; h < kCols; h += 16)
+          ptx::tmem_ld_32x32b_x16(base + c + h, *reinterpret_cast<uint32_t(*)[16]>(v + h));
+        ptx::tmem_wait_ld();
+        // whole chunks: rows past the last token stay inside the T rows of the tile
+#pragma unroll
+        for (int e = 0; e < kCols; ++e)
+          if (SVDQ_IN_SMEM(smem_raw, part + (c + e) * kRowsW, 4, p.err))
+            part[(c + e) * kRowsW] = __uint_as_float(v[e]);
       }
       ptx::tc_fence_before();
     }
@@ -260,43 +258,46 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
 
+  if (ks > 1 && warp < kEpiWarp0) ptx::cluster_wait();       // the epilogue warps have waited
+  __syncthreads();                                           // this CTA's own rows lie in its ring
+  bool ok = *abort_flag == 0;
   if (ks > 1) {
-    if (warp < kEpiWarp0) ptx::cluster_wait();       // the epilogue warps have waited
-    // The partial sums are added in CTA order; a thread takes two neighbouring columns of a token.
-    // This CTA's own rows lie in its ring: written by its epilogue warps, which the barrier orders.
-    __syncthreads();
-    const bool ok = wait_bounded(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal);
+    ok = wait_bounded(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
     // what the others sent has arrived; when all CTAs say so, every copy has left its source
     __syncwarp();
     ptx::cluster_arrive();
-    if (ok) {
-      const int col = 2 * (threadIdx.x & 63);
-      float b0 = 0.f, b1 = 0.f;
-      if (p.bias) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n0 + col));
-        b0 = __uint_as_float(w << 16);
-        b1 = __uint_as_float(w & 0xFFFF0000u);
-      }
-      const float* mine = reinterpret_cast<const float*>(smem) + split * share * kRowsW + col;
-      for (int i = threadIdx.x >> 6; i < own; i += kThreads / 64) {
-        float2 a = make_float2(0.f, 0.f);
-        for (int r = 0; r < ks; ++r) {
-          const float* src = r == split ? mine + i * kRowsW : red + (r * share + i) * kRowsW + col;
-          if (!SVDQ_IN_SMEM(smem_raw, src, 8, p.err)) continue;
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          a.x += v.x;
-          a.y += v.y;
-        }
-        if (SVDQ_IN_GLOBAL(n0 + col + 2 <= p.N, p.err))
-          *reinterpret_cast<__nv_bfloat162*>(p.Y + static_cast<size_t>(m0 + split * share + i) * p.N + n0 + col) =
-              __floats2bfloat162_rn(a.x + b0, a.y + b1);
-      }
-    }
-    __syncwarp();
-    ptx::cluster_wait();
-  } else {
-    __syncthreads();
   }
+  // The partial sums are added in CTA order; a warp takes a token, a thread four columns.
+  if (ok) {
+    const int col = 4 * (threadIdx.x & 31);
+    float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.bias) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.bias + n0 + col));
+      b = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                      __uint_as_float(w.y & 0xFFFF0000u));
+    }
+    const float* mine = reinterpret_cast<const float*>(smem) + split * share * kRowsW + col;
+#pragma unroll 2
+    for (int i = warp; i < own; i += kThreads / 32) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int r = 0; r < ks; ++r) {
+        const float* src = r == split ? mine + i * kRowsW : red + (r * share + i) * kRowsW + col;
+        if (!SVDQ_IN_SMEM(smem_raw, src, 16, p.err)) continue;
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x + b.x, a.y + b.y), hi = __floats2bfloat162_rn(a.z + b.z, a.w + b.w);
+      if (SVDQ_IN_GLOBAL(n0 + col + 4 <= p.N, p.err))
+        *reinterpret_cast<uint2*>(p.Y + static_cast<size_t>(m0 + split * share + i) * p.N + n0 + col) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+  }
+  __syncwarp();
+  if (ks > 1) ptx::cluster_wait();
   if (warp == kMmaWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::kTmemCols);
@@ -304,15 +305,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <int T>
-constexpr size_t smem_bytes() {
-  return 1024 + Cfg<T>::kStages * Cfg<T>::kStageBytes + kSfBufs * 2 * kSfBlk + Cfg<T>::kRedBytes + sizeof(SharedTail<T>);
+constexpr size_t smem_bytes(int stages = Cfg<T>::kStages) {
+  return 1024 + stages * Cfg<T>::kStageBytes + kSfBufs * 2 * kSfBlk + Cfg<T>::kRedBytes + sizeof(SharedTail<T>);
 }
 
 template <int T>
-void fill_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int clusters, int ks, cudaStream_t s) {
+void fill_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int clusters, int ks, int stages,
+                 cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(clusters) * static_cast<unsigned>(ks), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes<T>();
+  cfg.dynamicSmemBytes = smem_bytes<T>(stages);
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
@@ -334,7 +336,7 @@ int resident_clusters(int ks) {
   if (known > 0) return known - 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  fill_config<T>(cfg, attr, 1, ks, nullptr);
+  fill_config<T>(cfg, attr, 1, ks, Cfg<T>::kStages, nullptr);
   cfg.numAttrs = 1;                                      // the cluster alone
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, gemm_fp8_small_kernel<T>, &cfg) != cudaSuccess) {
@@ -348,10 +350,8 @@ int resident_clusters(int ks) {
 template <int T>
 cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw, const CUtensorMap& tsfx,
                    const CUtensorMap& tl2, const CUtensorMap& tz, GemmParams p, cudaStream_t s) {
-  static_assert((T < 128 ? 2 : 1) * (smem_bytes<T>() + 1024) <= 228 * 1024, "shared memory of an SM");
+  static_assert(smem_bytes<T>() <= 232448, "shared memory of one CTA");
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(gemm_fp8_small_kernel<T>), smem_bytes<T>());
-  if (e != cudaSuccess) return e;
-  e = prefer_max_shared_once(reinterpret_cast<const void*>(gemm_fp8_small_kernel<T>));
   if (e != cudaSuccess) return e;
   // The widest split with every cluster resident at once: a second wave costs a whole pass.
   const int nk = p.K / kKTile;
@@ -363,7 +363,14 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorM
     }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  fill_config<T>(cfg, attr, p.num_tiles, p.ksplit, s);
+  // A ring no longer than a CTA's steps, and no deeper than 12 MB in flight over all CTAs need (1.5 us
+  // of latency at 8 TB/s): a smaller CTA leaves the next launch room to set itself up.
+  const int steps = (nk + p.ksplit - 1) / p.ksplit + (p.rank + 63) / 64;
+  const int64_t deep = (int64_t(12) << 20) / (int64_t(p.num_tiles) * p.ksplit * Cfg<T>::kStageBytes) + 1;
+  p.stages = steps < deep ? steps : static_cast<int>(deep);
+  if (p.stages < Cfg<T>::kMinStages) p.stages = Cfg<T>::kMinStages;
+  if (p.stages > Cfg<T>::kStages) p.stages = Cfg<T>::kStages;
+  fill_config<T>(cfg, attr, p.num_tiles, p.ksplit, p.stages, s);
   e = cudaLaunchKernelEx(&cfg, gemm_fp8_small_kernel<T>, tw, tx, tsfw, tsfx, tl2, tz, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

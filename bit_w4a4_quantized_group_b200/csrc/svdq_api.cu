@@ -90,38 +90,28 @@ bool make_tmap_sf8(CUtensorMap* m, const void* base, int64_t rows_pad, int64_t K
 
 }  // namespace
 
-namespace {
-// Function attributes already set: (kernel, device, attribute, value) seen by set_once.
-cudaError_t set_once(const void* kernel, cudaFuncAttribute attr, int value) {
+cudaError_t set_smem_limit_once(const void* kernel, size_t smem) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   struct Seen {
     const void* kernel;
-    int dev, attr, value;
+    int dev;
+    size_t smem;
   };
-  static Seen seen[1024];
+  static Seen seen[512];
   static int n = 0;
   static std::mutex mu;
   {
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < n; ++i)
-      if (seen[i].kernel == kernel && seen[i].dev == dev && seen[i].attr == attr && seen[i].value == value)
-        return cudaSuccess;
+      if (seen[i].kernel == kernel && seen[i].dev == dev && seen[i].smem == smem) return cudaSuccess;
   }
-  e = cudaFuncSetAttribute(kernel, attr, value);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
-  if (n < 1024) seen[n++] = Seen{kernel, dev, static_cast<int>(attr), value};
+  if (n < 512) seen[n++] = Seen{kernel, dev, smem};
   return cudaSuccess;
-}
-}  // namespace
-
-cudaError_t set_smem_limit_once(const void* kernel, size_t smem) {
-  return set_once(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-}
-cudaError_t prefer_max_shared_once(const void* kernel) {
-  return set_once(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
 }
 
 namespace {

@@ -118,9 +118,6 @@ cudaError_t launch_selftest_bounded_wait(int* err, uint64_t limit_ns, cudaStream
 // per (kernel, device, size): the attribute belongs to the function in the device's context,
 // and setting it on every launch costs host time.
 cudaError_t set_smem_limit_once(const void* kernel, size_t smem);
-// Asks for the largest shared-memory share of the SM's on-chip memory, once per (kernel, device):
-// without it the driver may leave room for one CTA of a kernel of which two would fit.
-cudaError_t prefer_max_shared_once(const void* kernel);
 
 struct ProParams {
   int M, K, rank, Mpad, stages;
@@ -148,6 +145,7 @@ struct GemmParams {
   int op_pair;               // FP4: A and B tensor maps are 3-D and load two K steps at once
   int y_align32;             // Y is 32-byte aligned (256-bit stores)
   int ksplit;                // INT4, FP8 with few tokens: CTAs of a cluster that split one tile's K steps (1: none)
+  int stages;                // FP8 with few tokens: slots of the ring
 };
 
 // Row kernels with an FP8 output; sfb = ceil(K/512) scale blocks per 128 rows.
