@@ -13,8 +13,11 @@
 //   * clusters of two CTAs compute 256 x BN output tiles with cta_group::2 MMAs, each CTA
 //     holding 128 rows of A and BN/2 rows of B; persistent clusters take contiguous runs of the
 //     N-fastest tile numbering;
-//   * a ring slot holds one K step of 128 bytes per row of A and B, counted on a barrier of the
-//     leader CTA (each CTA loads into its own shared memory; no multicast loads);
+//   * a ring slot holds two K steps of 128 bytes per row of A and B, each operand brought by one 3-D
+//     TMA load ([K/128 chunks][rows][128 bytes], two chunks per box) and counted on a barrier of the
+//     leader CTA (each CTA loads into its own shared memory; no multicast loads).  The MMA warp's
+//     own work per slot (waits, issue, commit) is of the order of 400 cycles, so that slots of one
+//     step kept the tensor pipe waiting: 512 cycles of MMAs at BN = 256, 128 at BN = 64;
 //   * the scale blocks (512 bytes per 128 rows and four steps) have a ring of their own: a copy
 //     warp of the leader moves them into the TMEM buffer of the same number (two or three
 //     tcgen05.cp per four steps) as they land, ahead of the MMA warp;
@@ -51,8 +54,8 @@ struct Cfg {
   static constexpr uint32_t kBBytes = kBRows * 128;
   static constexpr int kSfbBlks = BN > 128 ? 2 : 1;                   // 128-row scale blocks a tile's columns touch
   static constexpr uint32_t kSfBytes = (1 + kSfbBlks) * kSfBlk;
-  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN >= 192 ? 6 : 8;                   // released two at a time
+  static constexpr uint32_t kStageBytes = 2 * (kABytes + kBBytes);     // [A step 0][A step 1][B step 0][B step 1]
+  static constexpr int kStages = BN >= 192 ? 3 : BN == 128 ? 4 : 5;
   static constexpr int kAccs = BN == 256 ? 1 : 2;                     // accumulators in TMEM
   static constexpr uint32_t kTmemSf0 = kAccs * BN;
   static constexpr int kColsPerWarp = BN / 2;                         // epilogue columns of a warp
@@ -73,8 +76,8 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
 
 template <int BN>
 struct SharedTail {
-  uint64_t full[Cfg<BN>::kStages];    // slot holds its step (TMA bytes of both CTAs)
-  uint64_t empty[Cfg<BN>::kStages / 2];   // the MMAs that read slots 2i and 2i + 1 have completed
+  uint64_t full[Cfg<BN>::kStages];    // slot holds its two steps (TMA bytes of both CTAs)
+  uint64_t empty[Cfg<BN>::kStages];   // the MMAs that read the slot have completed
   uint64_t sf_full[kSfBufs];          // scale slot holds the blocks of four steps (TMA bytes of both CTAs)
   uint64_t sf_ready[kSfBufs];         // ... and so does the TMEM buffer of the same number
   uint64_t sf_free[kSfBufs];          // the MMAs that read the TMEM buffer have completed
@@ -103,13 +106,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cluster = blockIdx.x >> 1;
   const int nclusters = gridDim.x >> 1;
   const int nk = p.K / kKTile;
-  const int nk_lr = (p.rank + 63) / 64;
+  const int nd = (nk + 1) / 2;                       // double steps: slots of the 8-bit product per tile
+  const int nk_lr = (p.rank + 63) / 64;              // ... and one per 64 columns of the branch
   const TileSeq tiles(p.num_tiles, p.tiles_n, cluster, nclusters);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(&sh->full[s], 1);
-      if ((s & 1) == 0) ptx::mbar_init(&sh->empty[s >> 1], 1);
+      ptx::mbar_init(&sh->empty[s], 1);
     }
     for (int b = 0; b < kSfBufs; ++b) {
       ptx::mbar_init(&sh->sf_full[b], 1);
@@ -146,40 +150,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::prefetch_tmap(&tmap_l2);
       }
       const uint64_t keep = ptx::l2_evict_last_policy();   // A and B tiles are re-read by other clusters
-      int it = 0, b = 0;
-      uint32_t sfph = 1;
+      int s = 0, b = 0;
+      uint32_t ph = 1, sfph = 1;
       bool ok = true;
       for (int j = 0; j < tiles.count && ok; ++j) {
         const int m0 = tiles.mb(j) * kBM + static_cast<int>(rank) * kRows;     // this CTA's A rows
         const int n0 = tiles.nb(j) * BN;
         const int nb0 = n0 + static_cast<int>(rank) * C::kBRows;               // this CTA's B rows
-        for (int k = 0; k < nk + nk_lr; ++k, ++it) {
-          const int s = it % C::kStages;
-          const uint32_t ph = (it / C::kStages) & 1;
-          if ((s & 1) == 0 && !wait_bounded(&sh->empty[s >> 1], ph ^ 1u, abort_flag, p.err, kErrSiteGemmEmpty)) {
-            ok = false;
-            break;
-          }
-          if (k < nk && (k & 3) == 0) {
+        for (int d = 0; d < nd + nk_lr; ++d) {
+          if (!wait_bounded(&sh->empty[s], ph, abort_flag, p.err, kErrSiteGemmEmpty)) { ok = false; break; }
+          if (d < nd && (d & 1) == 0) {
             // the scale blocks of the next four steps
             if (!wait_bounded(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree)) { ok = false; break; }
             const uint32_t sf_leader = ptx::mapa_shared(ptx::smem_u32(&sh->sf_full[b]), 0);
             const uint32_t sf = ptx::smem_u32(sf_smem + b * C::kSfBytes);
             if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->sf_full[b], 2 * C::kSfBytes);
-            ptx::tma_load_3d_pair_hint(sf, &tmap_sfa, sf_leader, 0, k >> 2, m0 >> 7, keep);
-            ptx::tma_load_3d_pair_hint(sf + kSfBlk, &tmap_sfb, sf_leader, 0, k >> 2, n0 >> 7, keep);
+            ptx::tma_load_3d_pair_hint(sf, &tmap_sfa, sf_leader, 0, d >> 1, m0 >> 7, keep);
+            ptx::tma_load_3d_pair_hint(sf + kSfBlk, &tmap_sfb, sf_leader, 0, d >> 1, n0 >> 7, keep);
             if (++b == kSfBufs) { b = 0; sfph ^= 1u; }
           }
           const uint32_t full_leader = ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0);
           const uint32_t st = ptx::smem_u32(smem + s * C::kStageBytes);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->full[s], 2 * C::kStageBytes);
-          if (k < nk) {
-            ptx::tma_load_2d_pair_hint(st, &tmap_a, full_leader, k * kKTile, m0, keep);
-            ptx::tma_load_2d_pair_hint(st + kABytes, &tmap_b, full_leader, k * kKTile, nb0, keep);
+          if (d < nd) {
+            // one load per operand: steps 2d and 2d + 1 (a missing second step reads as zeros)
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->full[s], 2 * C::kStageBytes);
+            ptx::tma_load_3d_pair_hint(st, &tmap_a, full_leader, 0, m0, 2 * d, keep);
+            ptx::tma_load_3d_pair_hint(st + 2 * kABytes, &tmap_b, full_leader, 0, nb0, 2 * d, keep);
           } else {
-            ptx::tma_load_2d_pair(st, &tmap_z, full_leader, (k - nk) * 64, m0);
-            ptx::tma_load_2d_pair(st + kABytes, &tmap_l2, full_leader, (k - nk) * 64, nb0);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->full[s], C::kStageBytes);
+            ptx::tma_load_2d_pair(st, &tmap_z, full_leader, (d - nd) * 64, m0);
+            ptx::tma_load_2d_pair(st + 2 * kABytes, &tmap_l2, full_leader, (d - nd) * 64, nb0);
           }
+          if (++s == C::kStages) { s = 0; ph ^= 1u; }
         }
       }
     }
@@ -201,35 +203,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t acc = tmem + static_cast<uint32_t>(a * BN);
         // a tile that starts inside a 128-row scale block (BN 64 and 192) skips the block's first columns
         const uint32_t sfb_skip = static_cast<uint32_t>((tiles.nb(j) * BN) & 127) / 32;
-        for (int k = 0; k < nk + nk_lr; ++k) {
+        for (int d = 0; d < nd + nk_lr; ++d) {
           if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) { ok = false; break; }
-          const bool main_step = k < nk;
-          const uint32_t id = static_cast<uint32_t>(k & 3);     // byte of the scale columns
-          if (main_step && id == 0 &&
+          const bool main_slot = d < nd;
+          if (main_slot && (d & 1) == 0 &&
               !wait_bounded(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const bool sf_done = main_step && (id == 3 || k == nk - 1);
-          const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
-          const uint32_t sfb = sfa + 4 + sfb_skip;
+          const bool sf_done = main_slot && ((d & 1) == 1 || d == nd - 1);
           if (ptx::elect_one()) {
             const uint64_t ad = desc0 + static_cast<uint64_t>(s) * (C::kStageBytes / 16);
-            const uint64_t bd = ad + kABytes / 16;
-            if (main_step) {
-              const uint32_t idesc = idesc_mxf8(kBM, BN, 0) | (id << 29) | (id << 4);
+            const uint64_t bd = ad + 2 * kABytes / 16;
+            if (main_slot) {
+              const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
+              const uint32_t sfb = sfa + 4 + sfb_skip;
+              const uint32_t id0 = static_cast<uint32_t>(d & 1) * 2;    // byte of the scale columns
 #pragma unroll
-              for (int q = 0; q < kKTile / 32; ++q)
-                ptx::umma_mxf8_pair(acc, ad + 2 * q, bd + 2 * q, idesc, sfa | (id << 30), sfb | (id << 30),
-                                    (k | q) != 0 ? 1u : 0u);
+              for (int h = 0; h < 2; ++h) {
+                if (h == 1 && 2 * d + 1 == nk) break;                   // an odd last step
+                const uint32_t id = id0 + h;
+                const uint32_t idesc = idesc_mxf8(kBM, BN, 0) | (id << 29) | (id << 4);
+#pragma unroll
+                for (int q = 0; q < kKTile / 32; ++q)
+                  ptx::umma_mxf8_pair(acc, ad + h * (kABytes / 16) + 2 * q, bd + h * (C::kBBytes / 16) + 2 * q, idesc,
+                                      sfa | (id << 30), sfb | (id << 30), (d | h | q) != 0 ? 1u : 0u);
+              }
               if (sf_done) ptx::tc_commit_pair(&sh->sf_free[b], 0x3);
             } else {
-              const int nmma = min(64, p.rank - (k - nk) * 64) / 16;
+              const int nmma = min(64, p.rank - (d - nd) * 64) / 16;
               for (int q = 0; q < nmma; ++q) ptx::umma_f16_pair(acc, ad + 2 * q, bd + 2 * q, id16, 1u);
             }
-            if (s & 1) ptx::tc_commit_pair(&sh->empty[s >> 1], 0x3);
-            if (k == nk + nk_lr - 1) ptx::tc_commit_pair(&sh->acc_full[a], 0x3);
+            ptx::tc_commit_pair(&sh->empty[s], 0x3);
+            if (d == nd + nk_lr - 1) ptx::tc_commit_pair(&sh->acc_full[a], 0x3);
           }
           __syncwarp();
           if (sf_done && ++b == kSfBufs) { b = 0; sfph ^= 1u; }
@@ -398,21 +405,21 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorM
 
 }  // namespace
 
-int gemm_fp8_tile_n(int M, int N, int num_sms) {
-  // The tile width with the least time: waves of the persistent clusters times the time of a K step,
-  // which fits 230 + width (in units of a column's time; measured at 4608 x 12288 x 3072, us a step:
-  // 0.52, 0.445, 0.385 and 0.313 for widths 256, 192, 128 and 64).
+float gemm_fp8_tile(int M, int N, int K, int num_sms, int* bn) {
+  // The tile width with the least time.  Waves of the persistent clusters times K steps times the time
+  // of a step, 0.13 us + 1.53 ns per column, and 4 us to start and drain.  Measured back to back, us a
+  // step for widths 256, 192, 128 and 64: 0.52, 0.43, 0.32 and 0.23 at 4608 x 12288 x 3072; whole calls
+  // 7.8 us at 300 x 2176 x 1152 (64 wide), 12.0 at 256 x 3072 x 9216 (128), 12.9 at 1024 x 3072 x 3072 (192).
   const int64_t tm = (M + kBM - 1) / kBM;
-  const int widths[4] = {256, 192, 128, 64};
-  int best = 256;
-  int64_t cost = INT64_MAX;
-  for (int w : widths) {
+  const int64_t slots = num_sms / 2 > 0 ? num_sms / 2 : 1;
+  float best = 0.f;
+  *bn = 0;
+  for (int w : {256, 192, 128, 64}) {
     const int64_t tiles = tm * ((N + w - 1) / w);
-    const int64_t slots = num_sms / 2;
-    const int64_t c = (tiles + slots - 1) / slots * (230 + w);
-    if (c < cost) {
-      cost = c;
-      best = w;
+    const float t = 4.f + static_cast<float>((tiles + slots - 1) / slots * (K / kKTile)) * (0.13f + 0.00153f * w);
+    if (*bn == 0 || t < best) {
+      best = t;
+      *bn = w;
     }
   }
   return best;

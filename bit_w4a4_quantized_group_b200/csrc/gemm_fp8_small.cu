@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* st = smem + s * C::kStageBytes;
         ptx::mbar_arrive_expect_tx(&sh->full[s], C::kStageBytes);
         if (k < nk) {
-          ptx::tma_load_2d(st, &tmap_w, &sh->full[s], (kb + k) * kKTile, n0);
-          ptx::tma_load_2d(st + kWBytes, &tmap_x, &sh->full[s], (kb + k) * kKTile, m0);
+          ptx::tma_load_3d(st, &tmap_w, &sh->full[s], 0, n0, kb + k);
+          ptx::tma_load_3d(st + kWBytes, &tmap_x, &sh->full[s], 0, m0, kb + k);
         } else {
           ptx::tma_load_2d(st, &tmap_l2, &sh->full[s], (k - nk) * 64, n0);
           ptx::tma_load_2d(st + kWBytes, &tmap_z, &sh->full[s], (k - nk) * 64, m0);
@@ -378,9 +378,23 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorM
 
 }  // namespace
 
-int gemm_fp8_small_tokens(int M) {
-  if (M > 128) return 0;
-  return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+int gemm_fp8_small_tokens(int M, int N, int K, int num_sms, float other_us) {
+  // Up to 64 tokens this kernel is the faster one (one token x 3072 x 9216: 7.7 us against 12; 64 x
+  // 3072 x 12288: 12.4 against 14).  Beyond, tiles of 128 tokens pay where the other kernel has few
+  // tiles and a long K: 4.3 us and 25 ns per token of a tile to start, add up and drain, and per K step 0.22 us or the time of
+  // 32 KB for every CTA at 8.6 TB/s (us measured, this kernel / the other: 128 x 12288 x 3072 15.9 / 26,
+  // 512 x 8192 x 512 10.9 / 19, 512 x 3072 x 9216 42 / 17).
+  if (M <= 64) return M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int64_t tiles = int64_t(N / kRowsW) * ((M + 127) / 128);
+  const int nk = K / kKTile;
+  int64_t ks = num_sms / tiles;
+  if (ks > kMaxSplit) ks = kMaxSplit;
+  if (ks > nk) ks = nk;
+  if (ks < 1) ks = 1;
+  const int64_t ctas = tiles * ks, waves = (ctas + num_sms - 1) / num_sms;
+  const float step = 0.0038f * static_cast<float>(ctas < num_sms ? ctas : num_sms);
+  const float us = 4.3f + 0.025f * static_cast<float>(M < 128 ? M : 128) + static_cast<float>(waves * ((nk + ks - 1) / ks)) * (step > 0.22f ? step : 0.22f);
+  return us < other_us ? 128 : 0;
 }
 
 cudaError_t launch_gemm_fp8_small(int tokens, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw,

@@ -343,8 +343,10 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
                         static_cast<cudaStream_t>(cuda_stream));
   } else if (fmt == SVDQ_FMT_FP8_G128) {
     // operand tiles of `xrows` tokens and `wrows` weights per CTA; a scale box spans `wblocks` row blocks
-    const int small = gemm_fp8_small_tokens(p.M);
-    const int bn = small ? 128 : gemm_fp8_tile_n(p.M, p.N, sms);
+    int bn = 0;
+    const float pair_us = gemm_fp8_tile(p.M, p.N, p.K, sms, &bn);
+    const int small = gemm_fp8_small_tokens(p.M, p.N, p.K, sms, pair_us);
+    if (small) bn = 128;
     const uint32_t xrows = small ? static_cast<uint32_t>(small) : 128u;
     const uint32_t wrows = small ? 128u : static_cast<uint32_t>(bn / 2);
     const uint32_t wblocks = !small && bn > 128 ? 2 : 1;
@@ -352,8 +354,14 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
     p.tiles_n = static_cast<int>((N + bn - 1) / bn);
     p.num_tiles = p.tiles_m * p.tiles_n;
     CUtensorMap ta, tb, tsfa, tsfb;
-    if (!make_tmap(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, M, 128, xrows)) return SVDQ_ERR_CUDA;
-    if (!make_tmap(&tb, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, 128, wrows)) return SVDQ_ERR_CUDA;
+    // rows seen as [K/128 steps][rows][128 bytes]; the large tiles load two steps per box
+    const uint32_t steps = small ? 1 : 2;
+    if (!make_tmap_3d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 128, M, K / 128, K, 128, 128, xrows, steps,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+      return SVDQ_ERR_CUDA;
+    if (!make_tmap_3d(&tb, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 128, N, K / 128, K, 128, 128, wrows, steps,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+      return SVDQ_ERR_CUDA;
     if (!make_tmap_sf8(&tsfa, a_scales, p.Mpad, K, 1)) return SVDQ_ERR_CUDA;
     if (!make_tmap_sf8(&tsfb, w_scales, p.Npad, K, wblocks)) return SVDQ_ERR_CUDA;
     if (rank > 0) {

@@ -191,14 +191,15 @@ size_t gemm_int4_smem_bytes();
 cudaError_t launch_gemm_w8a8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tz,
                              const CUtensorMap& tl2, const CUtensorMap& ty, const GemmParams& p, int num_sms,
                              cudaStream_t s);
-// FP8 GEMM: CTA-pair tiles of 256 x bn, bn = gemm_fp8_tile_n(...) in {64, 128, 192, 256}.
-int gemm_fp8_tile_n(int M, int N, int num_sms);
+// FP8 GEMM: CTA-pair tiles of 256 x bn.  gemm_fp8_tile picks bn (64, 128, 192 or 256) and returns the
+// estimated time in us.
+float gemm_fp8_tile(int M, int N, int K, int num_sms, int* bn);
 cudaError_t launch_gemm_fp8(int bn, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsfa,
                             const CUtensorMap& tsfb, const CUtensorMap& tz, const CUtensorMap& tl2,
                             const GemmParams& p, int num_sms, cudaStream_t s);
-// The same for few tokens: tiles of 128 weight rows x `tokens` (16, 32, 64 or 128; 0: use the kernel
-// above), K split over clusters (the launch picks p.ksplit).
-int gemm_fp8_small_tokens(int M);
+// The same for few tokens: tiles of 128 weight rows x `tokens` (16, 32, 64 or 128; 0: the kernel above,
+// which takes other_us, is the faster one), K split over clusters (the launch picks p.ksplit).
+int gemm_fp8_small_tokens(int M, int N, int K, int num_sms, float other_us);
 cudaError_t launch_gemm_fp8_small(int tokens, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw,
                                   const CUtensorMap& tsfx, const CUtensorMap& tl2, const CUtensorMap& tz,
                                   const GemmParams& p, cudaStream_t s);
