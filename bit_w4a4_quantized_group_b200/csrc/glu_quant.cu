@@ -6,12 +6,14 @@
 // form of GELU with t = 2 sqrt(2/pi) (x + 0.044715 x^3), since 1 + tanh(u) = 2 / (1 + exp(-2u)).
 // This form has no cancellation for negative x, and its ends are right without a branch: exp
 // overflows to infinity, whose reciprocal is 0, or underflows to 0 and leaves x.  exp and the
-// reciprocal are the hardware's approximations (2 and 1 units in the last place); a divide by
-// lambda is a product with its reciprocal.  All of it is far inside the E4M3 step of 2^-4.
+// reciprocal are the hardware's approximations (2 and 1 units in the last place); the divide by
+// lambda shares the reciprocal, 1 / ((1 + exp(-t)) lambda).  All of it is far inside the E4M3 step of 2^-4.
 //
-// What bounds it: memory (3 bytes per element, 5 with gating).  A thread holds 8 elements (16
-// bytes of each input) of kRows rows of the same columns, so that all its loads are in flight
-// together and lambda is read once per kRows rows; 16 lanes hold a group.
+// What bounds it: memory (3 bytes per element, 5 with gating).  Eight lanes hold a group: a
+// thread has two 16-byte chunks of it (64 elements apart, so that the lanes of a load are
+// neighbours) in each of kRows rows, all its loads in flight together.  The exponentials and
+// reciprocals (two per element, 16 a clock and SM) and the instruction issue are each busy about as
+// long as memory, so products run on pairs (f32x2) and row overheads are spread over 16 elements.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -25,18 +27,22 @@ namespace svdq {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = 4;
+constexpr int kGroups = kThreads / 8;          // 128-element groups across a CTA
+constexpr int kRows = 2;
 
-// 1 + exp(-t); the factors of t carry -log2(e), so that exp is one ex2.
+// -t log2(e) of a pair: the factor -log2(e) is folded into the constants, so that exp(-t) is one ex2.
 template <int ACT>
-__device__ __forceinline__ float act_denominator(float x) {
-  constexpr float kLog2e = 1.4426950408889634f, kC1 = 2.f * 0.7978845608028654f, kC3 = kC1 * 0.044715f;
-  const float t = ACT == SVDQ_ACT_SILU ? x * -kLog2e : x * fmaf(x * x, -kC3 * kLog2e, -kC1 * kLog2e);
+__device__ __forceinline__ float2 neg_t_log2(float2 x) {
+  constexpr float kLog2e = 1.4426950408889634f, kC1 = -2.f * 0.7978845608028654f * kLog2e, kC3 = kC1 * 0.044715f;
+  if (ACT == SVDQ_ACT_SILU) return __fmul2_rn(x, make_float2(-kLog2e, -kLog2e));
+  return __fmul2_rn(x, __ffma2_rn(__fmul2_rn(x, x), make_float2(kC3, kC3), make_float2(kC1, kC1)));
+}
+__device__ __forceinline__ float ex2_approx(float t) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-  return 1.f + e;
+  return e;
 }
-__device__ __forceinline__ float rcp_approx_ftz(float x) {
+__device__ __forceinline__ float rcp_approx(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
@@ -47,53 +53,97 @@ __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int t = static_cast<int>(threadIdx.x);
-  const int nc = p.K >> 3;
-  const int cblocks = (nc + kThreads - 1) / kThreads;
-  const int rb = static_cast<int>(blockIdx.x / static_cast<unsigned>(cblocks));
-  const int c = static_cast<int>(blockIdx.x % static_cast<unsigned>(cblocks)) * kThreads + t;
-  const int row0 = rb * kRows;
+  const int G = p.K >> 7;
+  const int cblocks = (G + kGroups - 1) / kGroups;
+  const int row0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(cblocks)) * kRows;
+  const int grp = static_cast<int>(blockIdx.x % static_cast<unsigned>(cblocks)) * kGroups + (t >> 3);
   if (row0 >= p.M) {      // the CTA behind the last row block
     fp8_zero_padding(p.scales, p.M, p.K, p.sfb, t, kThreads);
     return;
   }
-  const bool on = c < nc;
-  const size_t nscale = static_cast<size_t>((p.M + 127) / 128 * 128) * 4 * p.sfb;
-  uint4 g[kRows], u[kRows];
+  const bool on = grp < G;
+  const int rows = min(kRows, p.M - row0);
+  const size_t col = static_cast<size_t>(grp) * 128 + (t & 7) * 8;     // and col + 64
+  uint4 g[kRows][2], u[GATED ? kRows : 1][2];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int row = row0 + i;
-    g[i] = on && row < p.M ? ld_global_v4_na(p.gate + static_cast<size_t>(row) * p.ldg + static_cast<size_t>(c) * 8)
-                           : make_uint4(0, 0, 0, 0);
-    if (GATED)
-      u[i] = on && row < p.M ? ld_global_v4_na(p.up + static_cast<size_t>(row) * p.ldu + static_cast<size_t>(c) * 8)
-                             : make_uint4(0, 0, 0, 0);
-  }
-  float lam[8];
-  if (LAM) {
-    const float4 l0 = on ? __ldg(reinterpret_cast<const float4*>(p.lam) + 2 * c) : make_float4(1.f, 1.f, 1.f, 1.f);
-    const float4 l1 = on ? __ldg(reinterpret_cast<const float4*>(p.lam) + 2 * c + 1) : make_float4(1.f, 1.f, 1.f, 1.f);
-    // reciprocals, used for kRows rows
-    lam[0] = __frcp_rn(l0.x); lam[1] = __frcp_rn(l0.y); lam[2] = __frcp_rn(l0.z); lam[3] = __frcp_rn(l0.w);
-    lam[4] = __frcp_rn(l1.x); lam[5] = __frcp_rn(l1.y); lam[6] = __frcp_rn(l1.z); lam[7] = __frcp_rn(l1.w);
-  }
-  const int G = p.K >> 7, pad = 4 * p.sfb - G;
+    const bool in = on && i < rows;
+    const __nv_bfloat16* src = p.gate + static_cast<size_t>(row0 + i) * p.ldg + col;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int row = row0 + i;
-    if (row >= p.M) break;                         // the same for every thread
-    const uint32_t gx[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
-    uint32_t ux[4] = {0, 0, 0, 0};
-    if (GATED) { ux[0] = u[i].x; ux[1] = u[i].y; ux[2] = u[i].z; ux[3] = u[i].w; }
-    float y[8];
+    for (int h = 0; h < 2; ++h) g[i][h] = in ? ld_global_v4_na(src + 64 * h) : make_uint4(0, 0, 0, 0);
+    if (GATED) {
+      const __nv_bfloat16* srcu = p.up + static_cast<size_t>(row0 + i) * p.ldu + col;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = e & 1 ? bf16x2_hi(gx[e >> 1]) : bf16x2_lo(gx[e >> 1]);
-      y[e] = x * rcp_approx_ftz(act_denominator<ACT>(x));
-      if (GATED) y[e] *= e & 1 ? bf16x2_hi(ux[e >> 1]) : bf16x2_lo(ux[e >> 1]);
-      if (LAM) y[e] *= lam[e];
+      for (int h = 0; h < 2; ++h) u[i][h] = in ? ld_global_v4_na(srcu + 64 * h) : make_uint4(0, 0, 0, 0);
     }
-    fp8_store_chunk(y, on, row, c, p.K, p.sfb, p.codes, p.scales, nscale, p.err);
-    if (c < pad) p.scales[fp8_sf_offset(row, G + c, p.sfb)] = 0;      // padding groups (c < 3)
+  }
+  // y of every row, and the scale byte that this thread's own elements need.  The byte grows with the
+  // absolute value, so the group's byte is the largest of its lanes': two rows' bytes go through one
+  // shuffle as 16-bit halves.
+  float2 y[kRows][8];
+  float amax[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) amax[i] = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float2 lam[4];
+    if (LAM) {
+      const float4* lp = reinterpret_cast<const float4*>(p.lam + (on ? col : 0) + 64 * h);
+      const float4 l0 = __ldg(lp), l1 = __ldg(lp + 1);
+      lam[0] = make_float2(l0.x, l0.y);
+      lam[1] = make_float2(l0.z, l0.w);
+      lam[2] = make_float2(l1.x, l1.y);
+      lam[3] = make_float2(l1.z, l1.w);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const uint32_t gx[4] = {g[i][h].x, g[i][h].y, g[i][h].z, g[i][h].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = make_float2(bf16x2_lo(gx[e]), bf16x2_hi(gx[e]));
+        const float2 nt = neg_t_log2<ACT>(x);
+        float2 d = __fadd2_rn(make_float2(ex2_approx(nt.x), ex2_approx(nt.y)), make_float2(1.f, 1.f));
+        if (LAM) d = __fmul2_rn(d, lam[e]);           // one reciprocal serves both divides
+        float2 v = __fmul2_rn(x, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+        if (GATED) {
+          const uint32_t ux[4] = {u[i][h].x, u[i][h].y, u[i][h].z, u[i][h].w};
+          v = __fmul2_rn(v, make_float2(bf16x2_lo(ux[e]), bf16x2_hi(ux[e])));
+        }
+        amax[i] = fmaxf(amax[i], fmaxf(fabsf(v.x), fabsf(v.y)));
+        y[i][4 * h + e] = v;
+      }
+    }
+  }
+  uint32_t sb[kRows / 2];
+#pragma unroll
+  for (int i = 0; i < kRows / 2; ++i) {
+    sb[i] = fp8_scale_byte(amax[2 * i]) | (fp8_scale_byte(amax[2 * i + 1]) << 16);
+#pragma unroll
+    for (int o = 1; o <= 4; o <<= 1) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
+  }
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (i >= rows) break;
+    const int row = row0 + i;
+    const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+    const float inv = fp8_inv_scale(b);
+    uint8_t* dst = p.codes + static_cast<size_t>(row) * p.K + col;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = __fmul2_rn(y[i][4 * h + e], make_float2(inv, inv));
+        q[e] = ptx::cvt_e4m3x2(v.x, v.y);
+      }
+      if (SVDQ_IN_GLOBAL(col + 64 * h + 8 <= static_cast<size_t>(p.K), p.err))
+        *reinterpret_cast<uint2*>(dst + 64 * h) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    }
+    if ((t & 7) == 0) p.scales[fp8_sf_offset(row, grp, p.sfb)] = static_cast<uint8_t>(b);
+    // the row's padding groups, by the lanes of its last group
+    if (grp == G - 1 && (t & 7) > 0 && (t & 7) < 4 * p.sfb - G + 1)
+      p.scales[fp8_sf_offset(row, G - 1 + (t & 7), p.sfb)] = 0;
   }
 }
 
@@ -108,7 +158,7 @@ cudaError_t launch(const GluParams& p, const cudaLaunchConfig_t& cfg) {
 }  // namespace
 
 cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s) {
-  const int64_t cblocks = (p.K / 8 + kThreads - 1) / kThreads;
+  const int64_t cblocks = (p.K / 128 + kGroups - 1) / kGroups;
   const int64_t grid = cblocks * ((p.M + kRows - 1) / kRows) + (p.M % 128 ? 1 : 0);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
