@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libsvdq.so")
@@ -142,15 +141,18 @@ def svdq_last_cuda_error() -> str:
 
 # ----------------------------------------------------------------- torch helpers
 
-def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+_C = None     # torch._C, once a helper has needed it
 
 
 def _stream():
     """Raw handle of torch's current stream on the current device.  Read without building a
     torch.cuda.Stream object (3 us), which would cost as much as the launch of a small call."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    global _C
+    if _C is None:
+        import torch
+        torch.cuda.current_device()            # initialises CUDA on first use
+        _C = torch._C
+    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
 
 
 def _check(st: int, what: str):
@@ -186,45 +188,80 @@ def quantize_act_lowrank_down_t(fmt, X, lam, act_gscale, L1, a_codes, a_scales, 
     """Device prologue on torch tensors (X [M, K] bf16, L1 [r, K] bf16 viewed as any 2-byte dtype).
     `stream` is a raw cudaStream_t handle; None means torch's current stream."""
     M, K = X.shape
-    rank = 0 if L1 is None else L1.shape[0]
-    st = svdq_quantize_act_lowrank_down(fmt, M, K, rank, _ptr(X), _ptr(lam), act_gscale, _ptr(L1),
-                                        _ptr(a_codes), _ptr(a_scales), _ptr(Z),
-                                        _stream() if stream is None else stream)
-    _check(st, "svdq_quantize_act_lowrank_down")
+    st = (_lib or load()).svdq_quantize_act_lowrank_down(
+        _fmt(fmt), M, K, 0 if L1 is None else L1.shape[0], X.data_ptr(), None if lam is None else lam.data_ptr(),
+        act_gscale, None if L1 is None else L1.data_ptr(), a_codes.data_ptr(), a_scales.data_ptr(),
+        None if Z is None else Z.data_ptr(), _stream() if stream is None else stream)
+    if st != SVDQ_OK:
+        raise SvdqError(st, "svdq_quantize_act_lowrank_down")
 
 
 def w4a4_gemm_lowrank_up_t(fmt, M, N, K, rank, a_codes, a_scales, act_gscale, w_codes, w_scales, w_gscale,
                            Z, L2, bias, Y, stream=None):
-    st = svdq_w4a4_gemm_lowrank_up(fmt, M, N, K, rank, _ptr(a_codes), _ptr(a_scales), act_gscale,
-                                   _ptr(w_codes), _ptr(w_scales), w_gscale, _ptr(Z), _ptr(L2), _ptr(bias),
-                                   _ptr(Y), _stream() if stream is None else stream)
-    _check(st, "svdq_w4a4_gemm_lowrank_up")
+    st = (_lib or load()).svdq_w4a4_gemm_lowrank_up(
+        _fmt(fmt), M, N, K, rank, a_codes.data_ptr(), a_scales.data_ptr(), act_gscale, w_codes.data_ptr(),
+        w_scales.data_ptr(), w_gscale, None if Z is None else Z.data_ptr(), None if L2 is None else L2.data_ptr(),
+        None if bias is None else bias.data_ptr(), Y.data_ptr(), _stream() if stream is None else stream)
+    if st != SVDQ_OK:
+        raise SvdqError(st, "svdq_w4a4_gemm_lowrank_up")
 
 
-def _rows(t, shape, like, name):
-    """(pointer, row stride in elements) of a matrix of that shape with contiguous rows, of the
-    type and on the device of `like`; (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if t is not like and (t.shape != shape or t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name}: expected {tuple(shape)} {like.dtype} on {like.device}, got "
+def _current_device() -> int:
+    global _C
+    if _C is None:
+        import torch
+        _C = torch._C
+    return _C._cuda_getDevice()
+
+
+def _row_ld(t, shape, dtype, dev, name):
+    """Row stride in elements of a matrix of a call: of that shape and type, on that device, its rows
+    contiguous (a single row's stride is its length)."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on device {dev}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     ld, step = t.stride()
     if step != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+    return ld if shape[0] > 1 else shape[1]
+
+
+def _column_vector(t, K, dev, name):
+    """Pointer of an fp32 [K] vector (gamma, lambda) on that device; None for None."""
+    if t is None:
+        return None
+    if t.element_size() != 4 or not t.is_floating_point() or t.shape != (K,) or t.get_device() != dev or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous float32 [{K}] on device {dev}, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    return t.data_ptr()
+
+
+def _first_matrix(t, name):
+    """(shape, type, device, row stride) of a call's first matrix, which must lie on the current CUDA
+    device: the library launches there."""
+    shape, dtype, dev = t.shape, t.dtype, t.get_device()
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return shape, dtype, dev, ld if shape[0] > 1 else shape[1]
 
 
 def rmsnorm_quantize_act_t(fmt, X, residual, gamma, eps, H, a_codes, a_scales, stream=None):
     """Residual addition + RMS norm + quantization on torch tensors: X, residual, H bf16 [M, K] (rows
     may be strided; residual and H may be None), gamma fp32 [K] or None."""
-    shape = X.shape
-    x, ldx = _rows(X, shape, X, "X")
-    r, ldr = _rows(residual, shape, X, "residual")
-    h, ldh = _rows(H, shape, X, "H")
-    st = load().svdq_rmsnorm_quantize_act(_fmt(fmt), shape[0], shape[1], x, ldx, r, ldr, _ptr(gamma), eps, h, ldh,
-                                          a_codes.data_ptr(), a_scales.data_ptr(),
-                                          _stream() if stream is None else stream)
+    shape, dtype, dev, ldx = _first_matrix(X, "X")
+    r = h = None
+    ldr = ldh = 0
+    if residual is not None:
+        ldr, r = _row_ld(residual, shape, dtype, dev, "residual"), residual.data_ptr()
+    if H is not None:
+        ldh, h = _row_ld(H, shape, dtype, dev, "H"), H.data_ptr()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"expected tensors on the current CUDA device, got one on {X.device}")
+    st = (_lib or load()).svdq_rmsnorm_quantize_act(
+        _fmt(fmt), shape[0], shape[1], X.data_ptr(), ldx, r, ldr, _column_vector(gamma, shape[1], dev, "gamma"), eps,
+        h, ldh, a_codes.data_ptr(), a_scales.data_ptr(), _stream() if stream is None else stream)
     if st != SVDQ_OK:
         raise SvdqError(st, "svdq_rmsnorm_quantize_act")
 
@@ -232,11 +269,15 @@ def rmsnorm_quantize_act_t(fmt, X, residual, gamma, eps, H, a_codes, a_scales, s
 def glu_quantize_act_t(fmt, act, gate, up, lam, a_codes, a_scales, stream=None):
     """act(gate) [* up] [/ lam] + quantization on torch tensors: act "silu" or "gelu" (tanh form), gate
     and up bf16 [M, K] (column slices of a wider tensor will do; up may be None), lam fp32 [K] or None."""
-    shape = gate.shape
-    g, ldg = _rows(gate, shape, gate, "gate")
-    u, ldu = _rows(up, shape, gate, "up")
-    st = load().svdq_glu_quantize_act(_fmt(fmt), ACTIVATIONS[act], shape[0], shape[1], g, ldg, u, ldu, _ptr(lam),
-                                      a_codes.data_ptr(), a_scales.data_ptr(),
-                                      _stream() if stream is None else stream)
+    code = ACTIVATIONS[act]
+    shape, dtype, dev, ldg = _first_matrix(gate, "gate")
+    u, ldu = None, 0
+    if up is not None:
+        ldu, u = _row_ld(up, shape, dtype, dev, "up"), up.data_ptr()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"expected tensors on the current CUDA device, got one on {gate.device}")
+    st = (_lib or load()).svdq_glu_quantize_act(
+        _fmt(fmt), code, shape[0], shape[1], gate.data_ptr(), ldg, u, ldu,
+        _column_vector(lam, shape[1], dev, "lam"), a_codes.data_ptr(), a_scales.data_ptr(), _stream() if stream is None else stream)
     if st != SVDQ_OK:
         raise SvdqError(st, "svdq_glu_quantize_act")

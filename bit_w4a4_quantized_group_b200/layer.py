@@ -85,6 +85,47 @@ class W4A4LowRankLinear:
                 raise B.SvdqError(st, f"layer forward (device wait site {site})")
         return Y
 
+    def _check_fp8_feed(self, what: str):
+        if self.fmt != "fp8" or self.rank != 0:
+            raise ValueError(f"{what} feeds fp8 layers without a low-rank branch (this one: {self.fmt}, rank {self.rank})")
+
+    def fold_gamma(self, gamma: torch.Tensor) -> torch.Tensor:
+        """gamma / lambda in fp32: the weight of the norm before this layer, with the layer's smoothing
+        folded in.  Made once, when the model is loaded."""
+        g = gamma.to(device=self.device, dtype=torch.float32)
+        return (g if self.lam is None else g / self.lam).contiguous()
+
+    def forward_normed(self, X: torch.Tensor, residual: Optional[torch.Tensor], gamma: torch.Tensor, eps: float = 1e-6,
+                       H: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Y = the layer applied to RMSnorm(X + residual) * gamma, in two launches: the norm writes the
+        layer's quantized input directly (fp8, rank 0).  `gamma` is fp32 [K] from fold_gamma (None: all
+        ones, for a layer without smoothing); H, if given, receives X + residual in bf16 (it may be
+        `residual` or X itself).  Like forward(), asynchronous on the current stream."""
+        self._check_fp8_feed("forward_normed")
+        if gamma is None and self.lam is not None:
+            raise ValueError("a layer with smoothing factors needs gamma from fold_gamma")
+        M = X.shape[0]
+        ws = self.workspace(M)
+        B.rmsnorm_quantize_act_t(self.fmt, X, residual, gamma, eps, H, ws["a_codes"], ws["a_scales"])
+        return self._gemm(M, Y)
+
+    def forward_activated(self, act: str, gate: torch.Tensor, up: Optional[torch.Tensor] = None,
+                          Y: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Y = the layer applied to act(gate) [* up], in two launches: the second layer of an MLP on the
+        first one's output (fp8, rank 0).  act is "silu" or "gelu" (tanh form); gate and up may be
+        column slices of one GEMM output."""
+        self._check_fp8_feed("forward_activated")
+        M = gate.shape[0]
+        ws = self.workspace(M)
+        B.glu_quantize_act_t(self.fmt, act, gate, up, self.lam, ws["a_codes"], ws["a_scales"])
+        return self._gemm(M, Y)
+
+    def _gemm(self, M: int, Y: Optional[torch.Tensor]) -> torch.Tensor:
+        if Y is None:
+            Y = torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device)
+        self.gemm_only(M, Y)
+        return Y
+
     def gemm_only(self, M: int, Y: torch.Tensor, rank: Optional[int] = None):
         """The fused GEMM alone on the current workspace (rank 0 drops the branch)."""
         ws = self.workspace(M)

@@ -146,3 +146,35 @@ def test_helpers_refuse_mismatched_tensors():
         B.glu_quantize_act_t("fp8", "silu", X, X[:, :128], None, buf, buf)
     with pytest.raises(KeyError):
         B.glu_quantize_act_t("fp8", "relu", X, None, None, buf, buf, 0)
+
+
+def test_helpers_refuse_column_vectors_of_another_type_or_length():
+    X = torch.zeros((4, 256), dtype=torch.bfloat16)
+    for bad in (torch.ones(256, dtype=torch.bfloat16), torch.ones(128), torch.ones(512)[::2], torch.ones(256, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            B._column_vector(bad, 256, -1, "gamma")
+    assert B._column_vector(None, 256, -1, "gamma") is None
+    with pytest.raises(ValueError, match="current CUDA device"):
+        B.glu_quantize_act_t("fp8", "silu", X, None, None, X, X, 0)
+
+
+def test_layer_refuses_to_be_fed_where_it_cannot():
+    from bit_w4a4_quantized_group_b200.layer import W4A4LowRankLinear
+    rng = np.random.default_rng(0)
+    prep = {"lam": np.ones(256, np.float32), "R_nk": rng.standard_normal((128, 256)).astype(np.float32), "act_gscale": 1.0}
+    X = torch.zeros((2, 256), dtype=torch.bfloat16)
+    for fmt, rank in (("fp8", 16), ("w8a8", 0), ("nvfp4", 0)):
+        prep["L1_rk"] = np.zeros((rank, 256), np.float32)
+        prep["L2_nr"] = np.zeros((128, rank), np.float32)
+        lin = W4A4LowRankLinear(fmt, 128, 256, P.pack(fmt, prep), prep["lam"], 1.0, device="cpu")
+        with pytest.raises(ValueError, match="without a low-rank branch"):
+            lin.forward_normed(X, None, torch.ones(256))
+        with pytest.raises(ValueError, match="without a low-rank branch"):
+            lin.forward_activated("silu", X)
+    prep["L1_rk"], prep["L2_nr"] = np.zeros((0, 256), np.float32), np.zeros((128, 0), np.float32)
+    lam = rng.uniform(0.5, 2, 256).astype(np.float32)
+    lin = W4A4LowRankLinear("fp8", 128, 256, P.pack("fp8", prep), lam, 1.0, device="cpu")
+    with pytest.raises(ValueError, match="fold_gamma"):
+        lin.forward_normed(X, None, None)
+    g = torch.from_numpy(rng.uniform(0.5, 2, 256)).to(torch.bfloat16)
+    assert torch.equal(lin.fold_gamma(g), g.float() / torch.from_numpy(lam))

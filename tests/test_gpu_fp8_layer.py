@@ -184,3 +184,151 @@ def test_layer_forward(M, N, K, rank):
     # Z may round to the next bf16 (its own test bounds it), so the whole layer is compared by norm:
     # bf16 rounds Y by at most 2^-8 and Z's flips move it by less than that
     assert np.linalg.norm(Y - ref["Y"]) <= 2.0 ** -8 * np.linalg.norm(ref["Y"])
+
+
+def _weights64(lin):
+    N, K = lin.N, lin.K
+    return F.dequantize(lin.w_codes.cpu().numpy().reshape(N, K), F.scales_of(lin.w_scales.cpu().numpy(), N, K))
+
+
+def _fed64(lin, M):
+    """The quantized input that the last call left in the layer's workspace, in 64 bits."""
+    ws = lin.workspace(M)
+    K = lin.K
+    return F.dequantize(ws["a_codes"].cpu().numpy().reshape(M, K), F.scales_of(ws["a_scales"].cpu().numpy(), M, K))
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_mlp_block(M, act):
+    """Norm with residual -> gate-up layer -> gated activation -> down layer, each operator fed by
+    the one before, against 64-bit forms of every step on the operands that the step was given."""
+    K, I = 640, 1152
+    up, _, bu = _layer(2 * I, K, 0, 3)
+    down, _, bd = _layer(K, I, 0, 4)
+    rng = np.random.default_rng(M)
+    X, R = O.bf16_rn(rng.standard_normal((M, K)) * 2), O.bf16_rn(rng.standard_normal((M, K)))
+    gamma = torch.from_numpy(rng.uniform(0.5, 1.5, K).astype(np.float32)).to(torch.bfloat16)
+    folded = up.fold_gamma(gamma)
+    Xd, Rd = dev_bf16(X), dev_bf16(R)
+    H = torch.empty_like(Xd)
+    U = up.forward_normed(Xd, Rd, folded, 1e-6, H)
+    Y = down.forward_activated(act, U[:, :I], U[:, I:])
+    check_device_error()
+    h = O.bf16_rn(X.astype(np.float64) + R.astype(np.float64))
+    assert np.array_equal(host_bf16(H), h)
+    y64 = F.rmsnorm64(h.astype(np.float64), folded.cpu().numpy(), 1e-6)
+    F.check_quantized(up.workspace(M)["a_codes"].cpu().numpy().reshape(M, K),
+                      F.scales_of(up.workspace(M)["a_scales"].cpu().numpy(), M, K), y64, 2.0 ** -19)
+
+    def gemm_check(lin, got, bias):
+        A, W, b = _fed64(lin, M), _weights64(lin), O.bf16_rn(bias).astype(np.float64)
+        ref, S = A @ W.T + b, np.abs(A) @ np.abs(W).T + np.abs(b)
+        assert np.all(np.abs(host_bf16(got) - ref) <= 2.0 ** -8 * np.abs(ref) + (lin.K / 32 + 1) * 2.0 ** -23 * S)
+    gemm_check(up, U, bu)
+    u = host_bf16(U).astype(np.float64)
+    a64 = F.act64(u[:, :I], act) * u[:, I:] / down.lam.double().cpu().numpy()
+    F.check_quantized(down.workspace(M)["a_codes"].cpu().numpy().reshape(M, I),
+                      F.scales_of(down.workspace(M)["a_scales"].cpu().numpy(), M, I), a64, 2.0 ** -15, 2.0 ** -110)
+    gemm_check(down, Y, bd)
+
+
+@pytest.mark.parametrize("M", [1, 70, 260])
+def test_mlp_block_replays_from_a_graph_and_on_another_stream(M):
+    K, I = 640, 1152
+    up, _, _ = _layer(2 * I, K, 0, 5)
+    down, _, _ = _layer(K, I, 0, 6)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    folded = up.fold_gamma(torch.ones(K))
+    X = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+    R = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+    H, U, Y = torch.empty_like(X), torch.empty((M, 2 * I), dtype=torch.bfloat16, device="cuda"), torch.empty_like(X)
+
+    def block():
+        up.forward_normed(X, R, folded, 1e-6, H, U)
+        down.forward_activated("silu", U[:, :I], U[:, I:], Y)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block()
+    torch.cuda.current_stream().wait_stream(side)
+    first = Y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        block()
+        block()                                  # twice: each launch may start under the one before
+    for i in range(4):
+        X.copy_(torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) * (1 + i))
+        Y.fill_(float("nan"))
+        graph.replay()
+        replayed = Y.clone()
+        Y.fill_(float("nan"))
+        block()
+        assert torch.equal(replayed.view(torch.int16), Y.view(torch.int16)), i
+    assert torch.isfinite(first).all()
+    check_device_error()
+    del graph
+
+
+def test_calls_back_to_back_keep_stream_order():
+    """Writers and readers of one workspace in turn, without a wait between: every GEMM reads what the
+    call before it wrote, and every writer waits for the GEMM before it."""
+    K, N = 1024, 512
+    lin, _, _ = _layer(N, K, 0, 8)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    gamma = lin.fold_gamma(torch.ones(K))
+    for M in (1, 100, 400):
+        Xs = [torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16) * (i + 1) for i in range(6)]
+        ref = []
+        for x in Xs:
+            ref.append((lin.forward_normed(x, None, gamma), lin.forward_activated("gelu", x), lin.forward(x)))
+            torch.cuda.synchronize()
+        Ys = [tuple(torch.empty((M, N), dtype=torch.bfloat16, device="cuda") for _ in range(3)) for _ in Xs]
+        for _ in range(5):
+            for x, y in zip(Xs, Ys):
+                lin.forward_normed(x, None, gamma, Y=y[0])
+                lin.forward_activated("gelu", x, Y=y[1])
+                lin.forward(x, y[2])
+        check_device_error()
+        for a, b in zip(ref, Ys):
+            for u, v in zip(a, b):
+                assert torch.equal(u.view(torch.int16), v.view(torch.int16))
+
+
+def test_two_streams_at_once():
+    """Two layers on two streams, many calls in flight: outputs equal the calls alone."""
+    la, _, _ = _layer(640, 1152, 0, 11)
+    lb, _, _ = _layer(2304, 640, 16, 12)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Xa = torch.randn((33, 1152), generator=g, device="cuda").to(torch.bfloat16)
+    Xb = torch.randn((500, 640), generator=g, device="cuda").to(torch.bfloat16)
+    ra, rb = la.forward_activated("silu", Xa).clone(), lb.forward(Xb).clone()
+    Ya, Yb = torch.empty_like(ra), torch.empty_like(rb)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(50):
+        with torch.cuda.stream(sa):
+            la.forward_activated("silu", Xa, Y=Ya)
+        with torch.cuda.stream(sb):
+            lb.forward(Xb, Yb)
+    check_device_error()
+    assert torch.equal(ra.view(torch.int16), Ya.view(torch.int16))
+    assert torch.equal(rb.view(torch.int16), Yb.view(torch.int16))
+
+
+def test_many_repeats_of_long_k_agree():
+    """Rings that wrap many times, with every CTA of the device busy: 60 repeats, bit for bit."""
+    for M, N, K in ((1, 9216, 4096), (33, 12288, 3072), (100, 3072, 8192), (600, 2304, 4096)):
+        g = torch.Generator(device="cuda").manual_seed(M)
+        a, sa, _ = _operand(M, K, g, 2)
+        w, sw, _ = _operand(N, K, g, 2)
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        first = None
+        for i in range(60):
+            Y.fill_(float("nan"))
+            B.w4a4_gemm_lowrank_up_t("fp8", M, N, K, 0, a, sa, 1.0, w, sw, 1.0, None, None, None, Y)
+            if first is None:
+                first = Y.clone()
+            assert torch.equal(first.view(torch.int16), Y.view(torch.int16)), (M, N, K, i)
+        check_device_error()
