@@ -21,10 +21,6 @@
 // and scales are local to their groups, and the Z partials of the CTAs are added by CTA 0
 // of the cluster through distributed shared memory, in CTA order (deterministic).
 //
-// FP8 (groups of 128): the two warps whose boxes make up a group exchange their rows' maxima
-// through shared memory before either forms codes; everything else is one pass as for the 4-bit
-// formats, and the divide by a power-of-two scale is an exact product.
-//
 // W8A8 (the 8-bit setting: one scale per token row over all of K) needs each row's
 // maximum before any code can be formed, so the kernel makes two passes over its rows:
 // the first forms X_hat, the Z products and the row maxima; the compute warps then
@@ -53,7 +49,6 @@
 #include <cuda_fp16.h>
 #include <cstdint>
 
-#include "fp8_quant.cuh"
 #include "ptx.cuh"
 #include "svdq_device.cuh"
 
@@ -128,11 +123,7 @@ __device__ __forceinline__ float div_code(float a, float b, float y) {
 }
 
 // Bytes of code staging per compute warp: 16 rows x 64 columns of 4-bit or 8-bit codes.
-__host__ __device__ constexpr int code_stage_bytes(int fmt) { return fmt == kFmtW8a8 || fmt == kFmtFp8 ? 1024 : 512; }
-// Floats of row maxima per compute warp (16 rows; FP8 exchanges them twice in flight), and FP8's
-// pair barriers per compute warp.
-__host__ __device__ constexpr int rmax_floats(int fmt) { return fmt == kFmtFp8 ? 32 : 16; }
-__host__ __device__ constexpr int pair_bar_bytes(int fmt) { return fmt == kFmtFp8 ? 4 : 0; }
+__host__ __device__ constexpr int code_stage_bytes(int fmt) { return fmt == kFmtW8a8 ? 1024 : 512; }
 __host__ __device__ constexpr int passes(int fmt) { return fmt == kFmtW8a8 ? 2 : 1; }
 
 template <int FMT, int RANK, bool SPLIT>
@@ -154,11 +145,9 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
   constexpr int NPASS = passes(FMT);
   uint8_t* cstage = reinterpret_cast<uint8_t*>(empty + S);          // NW warps x CSTB code staging
   float* rmax_s = reinterpret_cast<float*>(cstage + NW * CSTB);     // W8A8: [BOXES][2 strips][16 rows]
-                                                                    // FP8: [2 in flight][BOXES][2][16]
-  float* rmax_cta = rmax_s + NW * rmax_floats(FMT);                   // W8A8 K split: this CTA's 32 row maxima
+  float* rmax_cta = rmax_s + BOXES * 32;                              // W8A8 K split: this CTA's 32 row maxima
   uint64_t* rm_bar = reinterpret_cast<uint64_t*>(rmax_cta + 32);      // ... published by every peer
-  uint64_t* px_bar = rm_bar + 1;                                      // FP8: one per pair of warps (NW / 2)
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(px_bar + NW * pair_bar_bytes(FMT) / 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(rm_bar + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -179,8 +168,6 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
       ptx::mbar_init(&empty[s], NW);
     }
     if (SPLIT && FMT == kFmtW8a8) ptx::mbar_init(rm_bar, static_cast<uint32_t>(p.ksplit - 1));
-    if (FMT == kFmtFp8)
-      for (int i = 0; i < NW / 2; ++i) ptx::mbar_init(&px_bar[i], 2);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -261,7 +248,6 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
     const float inv_gs = 1.0f / gs;     // exact: gs is a power of two
     constexpr float kRcp6 = 1.0f / 6.0f, kRcp7 = 1.0f / 7.0f;
     bool ok = true;
-    uint32_t npx = 0;                   // FP8: exchanges of row maxima so far
     // W8A8: running max |x_hat| of rows row_a / row_b over this warp's boxes (first pass), then
     // the row scales as divisors for the second pass: x_hat / s is formed as (x_hat f) / (s f)
     // with f = 2^64 for scales below 2^-64 (exact), so that RN(1 / (s f)) stays finite
@@ -492,58 +478,6 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
               }
             }
           }
-        } else if (FMT == kFmtFp8) {
-          // a 128-element group spans the boxes of two warps (phases 2i and 2i + 1 of one strip):
-          // they exchange their rows' maxima through shared memory.  Two buffers suffice, since a
-          // warp can be at most one exchange ahead of its partner.
-          float ma = 0.f, mb = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ma = fmaxf(ma, fmaxf(fmaxf(fabsf(nx[j][0].x), fabsf(nx[j][0].y)), fmaxf(fabsf(nx[j][1].x), fabsf(nx[j][1].y))));
-            mb = fmaxf(mb, fmaxf(fmaxf(fabsf(nx[j][2].x), fabsf(nx[j][2].y)), fmaxf(fabsf(nx[j][3].x), fabsf(nx[j][3].y))));
-          }
-          ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
-          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-          ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 2));
-          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
-          float* mine = rmax_s + (((npx & 1u) * BOXES + phase) * 2 + strip) * 16;
-          const float* theirs = rmax_s + (((npx & 1u) * BOXES + (phase ^ 1)) * 2 + strip) * 16;
-          uint64_t* pbar = &px_bar[(phase >> 1) * 2 + strip];
-          if (tig == 0) {
-            mine[g] = ma;
-            mine[g + 8] = mb;
-          }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(pbar);
-          if (!wait_bounded(pbar, npx & 1u, abort_flag, p.err, kErrSiteProPair)) { ok = false; break; }
-          ++npx;
-          ma = fmaxf(ma, theirs[g]);
-          mb = fmaxf(mb, theirs[g + 8]);
-          const uint32_t ba = fp8_scale_byte(ma), bb = fp8_scale_byte(mb);
-          // the product of -x_hat with -2^-e is x_hat / 2^e exactly
-          const float na = -fp8_inv_scale(ba), nb = -fp8_inv_scale(bb);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int pi = 0; pi < 4; ++pi) {
-              const float n = pi >= 2 ? nb : na;
-              const float2 q = __fmul2_rn(nx[j][pi], make_float2(n, n));
-              *reinterpret_cast<uint16_t*>(cst + (pi >= 2 ? g + 8 : g) * 64 + j * 16 + (pi & 1) * 8 + 2 * tig) =
-                  static_cast<uint16_t>(ptx::cvt_e4m3x2(q.x, q.y));
-            }
-          }
-          if (tig == 0 && (phase & 1) == 0) {
-            const int sfb = (p.K + 511) >> 9, grp = col0 >> 7, G = p.K >> 7;
-            uint8_t* sc = reinterpret_cast<uint8_t*>(p.scales);
-            if (SVDQ_IN_GLOBAL(grp < G && row_b < p.Mpad, p.err)) {
-              sc[fp8_sf_offset(row_a, grp, sfb)] = static_cast<uint8_t>(ba);
-              sc[fp8_sf_offset(row_b, grp, sfb)] = static_cast<uint8_t>(bb);
-              for (int z = grp + 1; grp == G - 1 && z < 4 * sfb; ++z) {      // padding groups
-                sc[fp8_sf_offset(row_a, z, sfb)] = 0;
-                sc[fp8_sf_offset(row_b, z, sfb)] = 0;
-              }
-            }
-          }
         } else {
           if (tig == 0) {
             // 4 consecutive E4M3 bytes of the 128x4 blocked layout per row
@@ -561,14 +495,14 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
           }
         }
         __syncwarp();
-        if (FMT != kFmtW8a8 && FMT != kFmtFp8) {
+        if (FMT != kFmtW8a8) {
           // 16 rows x 32 bytes of codes -> global, one 16-byte segment per lane
           const int r = lane >> 1, h = lane & 1;
           const int row = m0 + strip * 16 + r;
           const uint4 v = *reinterpret_cast<const uint4*>(cst + r * 32 + h * 16);
           if (row < p.M && SVDQ_IN_GLOBAL(col0 / 2 + h * 16 + 16 <= K2, p.err))
             *reinterpret_cast<uint4*>(p.codes + static_cast<size_t>(row) * K2 + col0 / 2 + h * 16) = v;
-        } else if (FMT == kFmtFp8 || pass == 1) {
+        } else if (pass == 1) {
           // 16 rows x 64 bytes of 8-bit codes -> global, two 16-byte segments per lane
           const int r = lane >> 1, h = lane & 1;
           const int row = m0 + strip * 16 + r;
@@ -740,15 +674,14 @@ size_t smem_bytes_for(int stages) {
   constexpr int NW = compute_warps(RANK);
   const ProSmemLayout L = pro_layout(RANK, NW / 2);
   return 1024 + static_cast<size_t>(stages) * L.stage_bytes + 2 * stages * 8 + NW * code_stage_bytes(FMT) +
-         NW * rmax_floats(FMT) * 4 + 32 * 4 + 8 + NW * pair_bar_bytes(FMT) + 16;
+         (NW / 2) * 32 * 4 + 32 * 4 + 8 + 16;
 }
 
 template <int FMT, int RANK>
 int stages_for() {
   constexpr int NW = compute_warps(RANK);
   const ProSmemLayout L = pro_layout(RANK, NW / 2);
-  const size_t budget = 220 * 1024 - 1024 - NW * code_stage_bytes(FMT) - NW * rmax_floats(FMT) * 4 - 32 * 4 - 8 -
-                        NW * pair_bar_bytes(FMT) - 64;
+  const size_t budget = 220 * 1024 - 1024 - NW * code_stage_bytes(FMT) - (NW / 2) * 32 * 4 - 32 * 4 - 8 - 64;
   int s = static_cast<int>(budget / L.stage_bytes);
   if (s > 4) s = 4;
   return s;
@@ -867,7 +800,6 @@ cudaError_t launch_prologue(int fmt, const CUtensorMap& tx, const CUtensorMap& t
   if (fmt == kFmtNvfp4) return launch_pro_rank<kFmtNvfp4>(tx, tl1, p, s);
   if (fmt == kFmtMxfp4) return launch_pro_rank<kFmtMxfp4>(tx, tl1, p, s);
   if (fmt == kFmtW8a8) return launch_pro_rank<kFmtW8a8>(tx, tl1, p, s);
-  if (fmt == kFmtFp8) return launch_pro_rank<kFmtFp8>(tx, tl1, p, s);
   return launch_pro_rank<kFmtInt4>(tx, tl1, p, s);
 }
 

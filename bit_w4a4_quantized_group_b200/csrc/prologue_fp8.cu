@@ -1,0 +1,511 @@
+// FP8 prologue: smoothing divide, quantization in groups of 128 and the low-rank down projection in
+// one read of X (svdq_quantize_act_lowrank_down with SVDQ_FMT_FP8_G128).
+//
+//   X_hat = bf16(X / lambda),  codes = e4m3(X_hat / 2^e),  Z = bf16(X_hat L1^T).
+//
+// The data flow is that of "SVDQuant 阅读笔记" §6.1 "算法 2" steps 1-3.  Two kernels:
+//
+// With a branch.  A CTA owns 128 rows and, in a cluster of up to 8 CTAs that split K, a share of the
+// 128-column groups.  TMA brings a group's X tile (two 128-byte-swizzled boxes of 64 columns) and
+// L1 rows into a ring.  Sixteen warps form X_hat from shared memory: 16 neighbouring lanes hold one
+// group of one row, so that a thread keeps its 8 columns' lambda in registers over all its rows, a
+// row's codes leave as 128 contiguous bytes, and the group maximum takes four shuffles for two rows
+// at once.  X_hat goes back to the place it came from, where the swizzle makes it the A operand of
+// the tensor core: tcgen05 kind::f16 MMAs (M = 128, N = rank) accumulate Z in TMEM over the CTA's
+// groups, so the branch costs the compute warps one 16-byte store per 8 elements.  The cluster's
+// partial Z tiles are added by the CTA that owns the rows, in CTA order (deterministic).
+//
+// Without a branch.  Nothing is shared between threads but the group maximum: plain 16-byte loads,
+// the same arithmetic, kRows rows of the same 8 columns per thread.
+//
+// What bounds them: memory in principle (3 bytes per element); the exact divide (five packed FMA-pipe
+// instructions per pair) and the conversions make the instruction issue nearly as busy.
+//
+// The divide x / lambda is the correctly rounded one (Markstein's two corrections, as in prologue.cu,
+// with y = RN(1 / lambda)); the sign of x is put back afterwards, since the corrections lose that of a
+// zero quotient in this order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <atomic>
+#include <cstdint>
+
+#include "fp8_quant.cuh"
+#include "ptx.cuh"
+#include "svdq_device.cuh"
+
+namespace svdq {
+namespace {
+
+// ------------------------------------------------------------------ arithmetic shared by both kernels
+// The divisors of a thread's 8 columns, as pairs: -lambda and RN(1 / lambda).
+struct Divisors {
+  float2 nb[4], y[4];
+};
+// X_hat of 8 elements: four bf16 pairs.
+template <bool LAM>
+__device__ __forceinline__ uint4 smooth8(uint4 v, const Divisors& d) {
+  if (!LAM) return v;                                  // x / 1
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 a = make_float2(bf16x2_lo(w[e]), bf16x2_hi(w[e]));
+    float2 q = __fmul2_rn(a, d.y[e]);
+    q = __ffma2_rn(__ffma2_rn(d.nb[e], q, a), d.y[e], q);
+    q = __ffma2_rn(__ffma2_rn(d.nb[e], q, a), d.y[e], q);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(q.x, q.y);
+    w[e] = (*reinterpret_cast<const uint32_t*>(&h) & 0x7FFF7FFFu) | (w[e] & 0x80008000u);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The scale byte that 8 elements need by themselves (the group's is the largest of its lanes').
+__device__ __forceinline__ uint32_t byte_of8(uint4 v) {
+  auto abs2 = [](uint32_t w) {
+    const uint32_t a = w & 0x7FFF7FFFu;
+    return *reinterpret_cast<const __nv_bfloat162*>(&a);
+  };
+  const __nv_bfloat162 m = __hmax2(__hmax2(abs2(v.x), abs2(v.y)), __hmax2(abs2(v.z), abs2(v.w)));
+  return fp8_scale_byte(fmaxf(__low2float(m), __high2float(m)));
+}
+__device__ __forceinline__ uint2 codes8(uint4 v, uint32_t byte) {
+  const float inv = fp8_inv_scale(byte);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __fmul2_rn(make_float2(bf16x2_lo(w[e]), bf16x2_hi(w[e])), make_float2(inv, inv));
+    q[e] = ptx::cvt_e4m3x2(f.x, f.y);
+  }
+  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+}
+
+// ------------------------------------------------------------------ without a branch
+constexpr int kQThreads = 128;
+constexpr int kQRows = 4;
+
+template <bool LAM>
+__global__ void __launch_bounds__(kQThreads) quantize_fp8_kernel(const __nv_bfloat16* X, ProParams p) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int t = static_cast<int>(threadIdx.x);
+  const int nc = p.K >> 3, G = p.K >> 7, sfb = (p.K + 511) >> 9;
+  const int cblocks = (nc + kQThreads - 1) / kQThreads;
+  const int row0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(cblocks)) * kQRows;
+  const int c = static_cast<int>(blockIdx.x % static_cast<unsigned>(cblocks)) * kQThreads + t;
+  uint8_t* scales = static_cast<uint8_t*>(p.scales);
+  if (row0 >= p.M) {      // the CTA behind the last row block
+    fp8_zero_padding(scales, p.M, p.K, sfb, t, kQThreads);
+    return;
+  }
+  const bool on = c < nc;
+  const int rows = min(kQRows, p.M - row0);
+  uint4 v[kQRows];
+#pragma unroll
+  for (int i = 0; i < kQRows; ++i)
+    v[i] = on && i < rows ? ld_global_v4_na(X + static_cast<size_t>(row0 + i) * p.K + static_cast<size_t>(c) * 8)
+                          : make_uint4(0, 0, 0, 0);
+  Divisors d;
+  if (LAM) {
+    const float4* lp = reinterpret_cast<const float4*>(p.lam) + (on ? 2 * c : 0);
+    const float4 l0 = __ldg(lp), l1 = __ldg(lp + 1);
+    const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      d.nb[e] = make_float2(-l[2 * e], -l[2 * e + 1]);
+      d.y[e] = make_float2(__frcp_rn(l[2 * e]), __frcp_rn(l[2 * e + 1]));
+    }
+  }
+  uint32_t sb[kQRows / 2];
+#pragma unroll
+  for (int i = 0; i < kQRows; ++i) {
+    v[i] = smooth8<LAM>(v[i], d);
+    const uint32_t b = byte_of8(v[i]);
+    sb[i / 2] = i & 1 ? sb[i / 2] | (b << 16) : b;
+  }
+#pragma unroll
+  for (int o = 1; o <= 8; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < kQRows / 2; ++i) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
+  }
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < kQRows; ++i) {
+    if (i >= rows) break;
+    const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+    if (SVDQ_IN_GLOBAL(c * 8 + 8 <= p.K, p.err))
+      *reinterpret_cast<uint2*>(p.codes + static_cast<size_t>(row0 + i) * p.K + static_cast<size_t>(c) * 8) = codes8(v[i], b);
+    if ((c & 15) == 0) scales[fp8_sf_offset(row0 + i, c >> 4, sfb)] = static_cast<uint8_t>(b);
+    if (c < 4 * sfb - G) scales[fp8_sf_offset(row0 + i, G + c, sfb)] = 0;       // padding groups (c < 3)
+  }
+}
+
+// ------------------------------------------------------------------ with a branch
+constexpr int kRowsP = 128;
+constexpr int kComputeWarps = 16;
+constexpr int kProdWarp = kComputeWarps, kMmaWarp = kComputeWarps + 1;
+constexpr int kThreadsP = 32 * (kComputeWarps + 2);
+constexpr uint32_t kXBytes = kRowsP * 256;              // two boxes of 128 rows x 64 bf16
+constexpr uint32_t kLamBytes = 1024;                    // lambda and RN(1 / lambda) of 128 columns
+constexpr int kMaxSplitP = 8;
+
+__host__ __device__ constexpr uint32_t idesc_bf16p(int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+// Padded row of a partial Z tile, in floats: 16 bytes more than the rank spread a column over the banks.
+__host__ __device__ constexpr int zrow(int rank) { return rank + 4; }
+__host__ __device__ constexpr uint32_t pstage_bytes(int rank) { return kXBytes + 256u * rank + kLamBytes; }
+__host__ __device__ constexpr uint32_t red_bytes(int rank) { return (kRowsP + kMaxSplitP - 1) * zrow(rank) * 4; }
+__host__ __device__ constexpr uint32_t ptmem_cols(int rank) { return rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+constexpr int kMaxStagesP = 5;
+
+struct PTail {
+  uint64_t full[kMaxStagesP];     // X and L1 tiles (TMA) and the divisors (the producer's lanes) are there
+  uint64_t xh_full[kMaxStagesP];  // X_hat has taken the place of X
+  uint64_t empty[kMaxStagesP];    // the MMAs that read the stage have completed
+  uint64_t acc_full;
+  uint64_t red_full;              // the other CTAs' partial Z of this CTA's rows have arrived
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <bool LAM>
+__global__ void __launch_bounds__(kThreadsP, 1)
+    prologue_fp8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_l1,
+                        ProParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int rank = p.rank, S = p.stages, ks = p.ksplit;
+  const uint32_t stage = pstage_bytes(rank);
+  float* red = reinterpret_cast<float*>(smem + S * stage);
+  PTail* sh = reinterpret_cast<PTail*>(smem + S * stage + (ks > 1 ? red_bytes(rank) : 0));
+  volatile int* abort_flag = &sh->abort_flag;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int split = static_cast<int>(blockIdx.x) % ks;
+  const int m0 = static_cast<int>(blockIdx.x) / ks * kRowsP;
+  const int G = p.K >> 7, sfb = (p.K + 511) >> 9;
+  const int gb = static_cast<int>(static_cast<int64_t>(G) * split / ks);                 // this CTA's groups
+  const int ng = static_cast<int>(static_cast<int64_t>(G) * (split + 1) / ks) - gb;      // >= 1: ks <= G
+  const int nrow = min(kRowsP, p.M - m0);
+  // K split: CTA r adds up the Z rows [r share, r share + own) of the block
+  const int share = (nrow + ks - 1) / ks;
+  const int own = max(0, min(share, nrow - split * share));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      ptx::mbar_init(&sh->full[s], 32);
+      ptx::mbar_init(&sh->xh_full[s], kComputeWarps);
+      ptx::mbar_init(&sh->empty[s], 1);
+    }
+    ptx::mbar_init(&sh->acc_full, 1);
+    ptx::mbar_init(&sh->red_full, 1);
+    sh->abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(&sh->tmem_base, ptmem_cols(rank));
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (ks > 1) {
+    if (threadIdx.x == 0)
+      ptx::mbar_arrive_expect_tx(&sh->red_full, static_cast<uint32_t>((ks - 1) * own * zrow(rank) * 4));
+    ptx::cluster_arrive();                // waited for before anything is sent: every CTA has started
+  }
+  const uint32_t tmem = sh->tmem_base;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+
+  if (warp == kProdWarp) {
+    // ------------------------------------------------------------ producer: tiles and divisors
+    if (lane == 0) {
+      ptx::prefetch_tmap(&tmap_x);
+      ptx::prefetch_tmap(&tmap_l1);
+    }
+    int s = 0;
+    uint32_t ph = 1;
+    // the next group's lambda is loaded while this one's tiles are on their way
+    float l[4] = {1.f, 1.f, 1.f, 1.f};
+    if (LAM)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[i] = __ldg(p.lam + gb * 128 + i * 32 + lane);
+    for (int g = 0; g < ng; ++g) {
+      if (!wait_bounded(&sh->empty[s], ph, abort_flag, p.err, kErrSiteProEmpty)) break;
+      uint8_t* st = smem + s * stage;
+      if (lane == 0) {
+        ptx::mbar_expect_tx(&sh->full[s], kXBytes + 256u * rank);
+        ptx::tma_load_3d(st, &tmap_x, &sh->full[s], 0, m0, 2 * (gb + g));
+        ptx::tma_load_3d(st + kXBytes, &tmap_l1, &sh->full[s], 0, 0, 2 * (gb + g));
+      }
+      if (LAM) {
+        float* ls = reinterpret_cast<float*>(st + kXBytes + 256 * rank);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (SVDQ_IN_SMEM(smem_raw, ls + 128 + i * 32 + lane, 4, p.err)) {
+            ls[i * 32 + lane] = l[i];
+            ls[128 + i * 32 + lane] = __frcp_rn(l[i]);
+          }
+        }
+        if (g + 1 < ng)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[i] = __ldg(p.lam + (gb + g + 1) * 128 + i * 32 + lane);
+      }
+      ptx::mbar_arrive(&sh->full[s]);        // each lane releases its own stores
+      if (++s == S) { s = 0; ph ^= 1u; }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ Z += X_hat L1^T
+    int s = 0;
+    uint32_t ph = 0;
+    const uint32_t idesc = idesc_bf16p(kRowsP, rank);
+    const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem));
+    for (int g = 0; g < ng; ++g) {
+      if (!wait_bounded(&sh->xh_full[s], ph, abort_flag, p.err, kErrSiteProPair)) break;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        const uint64_t ad = desc0 + static_cast<uint64_t>(s) * (stage / 16);
+        const uint64_t bd = ad + kXBytes / 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            ptx::umma_f16(tmem, ad + h * (kXBytes / 32) + 2 * q, bd + static_cast<uint64_t>(h) * (8 * rank) + 2 * q,
+                          idesc, (g | h | q) != 0 ? 1u : 0u);
+        ptx::tc_commit(&sh->empty[s]);
+        if (g == ng - 1) ptx::tc_commit(&sh->acc_full);
+      }
+      __syncwarp();
+      if (++s == S) { s = 0; ph ^= 1u; }
+    }
+  } else {
+    // ------------------------------------------------------------ compute warps: 8 rows of every tile each
+    const int c = lane & 15;                               // 16-byte chunk of the 128-column group
+    const int r0 = warp * 8 + (lane >> 4);                 // rows r0, r0 + 2, r0 + 4, r0 + 6
+    uint8_t* scales = static_cast<uint8_t*>(p.scales);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int g = 0; g < ng; ++g) {
+      if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteProFull)) break;
+      uint8_t* st = smem + s * stage;
+      Divisors d;
+      if (LAM) {
+        const float4* ls = reinterpret_cast<const float4*>(st + kXBytes + 256 * rank) + 2 * c;
+        const float4 l0 = ls[0], l1 = ls[1], y0 = ls[32], y1 = ls[33];
+        d.nb[0] = make_float2(-l0.x, -l0.y);
+        d.nb[1] = make_float2(-l0.z, -l0.w);
+        d.nb[2] = make_float2(-l1.x, -l1.y);
+        d.nb[3] = make_float2(-l1.z, -l1.w);
+        d.y[0] = make_float2(y0.x, y0.y);
+        d.y[1] = make_float2(y0.z, y0.w);
+        d.y[2] = make_float2(y1.x, y1.y);
+        d.y[3] = make_float2(y1.z, y1.w);
+      }
+      uint4 v[4];
+      uint32_t sb[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 2 * i;
+        uint8_t* at = st + (c >> 3) * (kXBytes / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        if (!SVDQ_IN_SMEM(smem_raw, at, 16, p.err)) at = st;
+        v[i] = smooth8<LAM>(*reinterpret_cast<const uint4*>(at), d);
+        if (LAM) *reinterpret_cast<uint4*>(at) = v[i];
+        const uint32_t b = byte_of8(v[i]);
+        sb[i / 2] = i & 1 ? sb[i / 2] | (b << 16) : b;
+      }
+      // X_hat is in place: hand the stage to the MMA warp before the codes are formed
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh->xh_full[s]);
+#pragma unroll
+      for (int o = 1; o <= 8; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
+      }
+      const int grp = gb + g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = m0 + r0 + 2 * i;
+        const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+        if (row < p.M && SVDQ_IN_GLOBAL(grp < G, p.err))
+          *reinterpret_cast<uint2*>(p.codes + static_cast<size_t>(row) * p.K + grp * 128 + c * 8) = codes8(v[i], b);
+        // rows past M read as zeros and get byte 0
+        if (c == 0) scales[fp8_sf_offset(row, grp, sfb)] = static_cast<uint8_t>(b);
+        if (grp == G - 1 && c > 0 && grp + c < 4 * sfb) scales[fp8_sf_offset(row, grp + c, sfb)] = 0;
+      }
+      if (++s == S) { s = 0; ph ^= 1u; }
+    }
+    if (warp < 4) {
+      // ---------------------------------------------------------- Z: thread = row, column = rank index
+      if (ks > 1) ptx::cluster_wait();
+      float* part = reinterpret_cast<float*>(smem);          // [row][zrow], in the drained ring
+      if (wait_bounded(&sh->acc_full, 0u, abort_flag, p.err, kErrSiteGemmAccFull)) {
+        ptx::tc_fence_after();
+        const int row = warp * 32 + lane;
+        const uint32_t base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll 1
+        for (int q = 0; q < rank; q += 16) {
+          uint32_t z[16];
+          ptx::tmem_ld_32x32b_x16(base + q, z);
+          ptx::tmem_wait_ld();
+          float4* dst = reinterpret_cast<float4*>(part + row * zrow(rank) + q);
+          if (SVDQ_IN_SMEM(smem_raw, dst, 64, p.err))
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_float4(__uint_as_float(z[4 * e]), __uint_as_float(z[4 * e + 1]),
+                                   __uint_as_float(z[4 * e + 2]), __uint_as_float(z[4 * e + 3]));
+        }
+        ptx::tc_fence_before();
+      }
+      if (ks > 1) {
+        // every other CTA gets its rows with one bulk copy
+        ptx::fence_proxy_async_smem();
+        named_barrier_sync(1, 128);
+        if (warp == 0 && lane < ks && lane != split && *abort_flag == 0) {
+          const int rows = min(share, nrow - lane * share);
+          if (rows > 0)
+            ptx::bulk_copy_to_cta(
+                ptx::mapa_shared(ptx::smem_u32(red + split * share * zrow(rank)), static_cast<uint32_t>(lane)),
+                part + lane * share * zrow(rank), static_cast<uint32_t>(rows * zrow(rank) * 4),
+                ptx::mapa_shared(ptx::smem_u32(&sh->red_full), static_cast<uint32_t>(lane)));
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  if (ks > 1 && warp >= 4) ptx::cluster_wait();              // warps 0-3 have waited
+  __syncthreads();
+  bool ok = *abort_flag == 0;
+  if (ks > 1) {
+    ok = wait_bounded(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
+    // what the others sent has arrived; when all CTAs say so, every copy has left its source
+    __syncwarp();
+    ptx::cluster_arrive();
+  }
+  if (ok) {
+    const float* mine = reinterpret_cast<const float*>(smem) + split * share * zrow(rank);
+    const int per = rank / 4;                                // threads of a row, four columns each
+    for (int i = threadIdx.x; i < own * per; i += kThreadsP) {
+      const int r = i / per, q = i % per * 4;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = 0; x < ks; ++x) {
+        const float* src = (x == split ? mine : red + x * share * zrow(rank)) + r * zrow(rank) + q;
+        if (!SVDQ_IN_SMEM(smem_raw, src, 16, p.err)) continue;
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
+      *reinterpret_cast<uint2*>(p.Z + static_cast<size_t>(m0 + split * share + r) * rank + q) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+  }
+  __syncwarp();
+  if (ks > 1) ptx::cluster_wait();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, ptmem_cols(rank));
+  }
+}
+
+size_t psmem(int rank, int stages, int ks) {
+  return 1024 + static_cast<size_t>(stages) * pstage_bytes(rank) + (ks > 1 ? red_bytes(rank) : 0) + sizeof(PTail);
+}
+// Stages that fit next to the partial sums; the ring also holds a CTA's own partial tile.
+int pstages(int rank, int ks) {
+  int s = kMaxStagesP;
+  while (s > 2 && psmem(rank, s, ks) > 232448) --s;
+  return s;
+}
+
+template <bool LAM>
+void fill_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int blocks, int ks, size_t smem,
+                 cudaStream_t s) {
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks) * static_cast<unsigned>(ks), 1, 1);
+  cfg.blockDim = dim3(kThreadsP, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+}
+
+// Clusters of ks CTAs that the current device holds at once (0 on error), asked once per device.
+template <bool LAM>
+int resident_clusters(int ks) {
+  static std::atomic<int> cache[64][kMaxSplitP + 1];     // 0: not asked yet, else 1 + the figure
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const int known = cache[dev][ks].load(std::memory_order_relaxed);
+  if (known > 0) return known - 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  fill_config<LAM>(cfg, attr, 1, ks, 232448, nullptr);
+  cfg.numAttrs = 1;                                      // the cluster alone
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, prologue_fp8_kernel<LAM>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  cache[dev][ks].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+template <bool LAM>
+cudaError_t launch_branch(const CUtensorMap& tx, const CUtensorMap& tl1, ProParams p, cudaStream_t s) {
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(prologue_fp8_kernel<LAM>), 232448);
+  if (e != cudaSuccess) return e;
+  const int blocks = p.Mpad / kRowsP, G = p.K / 128;
+  // the widest K split with every cluster resident at once
+  p.ksplit = 1;
+  for (int ks = G < kMaxSplitP ? G : kMaxSplitP; ks > 1; --ks)
+    if (resident_clusters<LAM>(ks) >= blocks) {
+      p.ksplit = ks;
+      break;
+    }
+  p.stages = pstages(p.rank, p.ksplit);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  fill_config<LAM>(cfg, attr, blocks, p.ksplit, psmem(p.rank, p.stages, p.ksplit), s);
+  e = cudaLaunchKernelEx(&cfg, prologue_fp8_kernel<LAM>, tx, tl1, p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prologue_fp8(const CUtensorMap& tx, const CUtensorMap& tl1, const ProParams& p, cudaStream_t s) {
+  return p.lam ? launch_branch<true>(tx, tl1, p, s) : launch_branch<false>(tx, tl1, p, s);
+}
+
+cudaError_t launch_quantize_fp8(const void* X, const ProParams& p, cudaStream_t s) {
+  const int64_t cblocks = (p.K / 8 + kQThreads - 1) / kQThreads;
+  const int64_t grid = cblocks * ((p.M + kQRows - 1) / kQRows) + (p.M % 128 ? 1 : 0);
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(kQThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(X);
+  cudaError_t e = p.lam ? cudaLaunchKernelEx(&cfg, quantize_fp8_kernel<true>, x, p)
+                        : cudaLaunchKernelEx(&cfg, quantize_fp8_kernel<false>, x, p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace svdq

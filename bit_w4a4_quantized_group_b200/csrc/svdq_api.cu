@@ -233,20 +233,6 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
   if (!is_pow2_positive(act_gscale)) return SVDQ_ERR_INVALID_ARG;
   if (fmt != SVDQ_FMT_NVFP4_G16 && act_gscale != 1.0f) return SVDQ_ERR_INVALID_ARG;
 
-  // X and L1 seen as [K/64 column blocks][rows][64 columns]: one load brings kProBoxes
-  // 64-column boxes (128B-swizzled) of 32 X rows or of all L1 rows
-  CUtensorMap tx, tl1;
-  const uint64_t rs = static_cast<uint64_t>(K) * 2;
-  if (!make_tmap_3d(&tx, X_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, M, K / 64, rs, 128, 64, 32, kProBoxes,
-                    CU_TENSOR_MAP_SWIZZLE_128B))
-    return SVDQ_ERR_CUDA;
-  if (rank > 0) {
-    if (!make_tmap_3d(&tl1, L1_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, rank, K / 64, rs, 128, 64, rank,
-                      kProBoxes, CU_TENSOR_MAP_SWIZZLE_128B))
-      return SVDQ_ERR_CUDA;
-  } else {
-    tl1 = tx;
-  }
   ProParams p{};
   p.M = static_cast<int>(M);
   p.K = static_cast<int>(K);
@@ -259,13 +245,33 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
   p.Z = static_cast<__nv_bfloat16*>(Z_bf16);
   p.err = device_error_word();
   if (!p.err) return SVDQ_ERR_CUDA;
-  const int kf = fmt == SVDQ_FMT_NVFP4_G16   ? kFmtNvfp4
-                 : fmt == SVDQ_FMT_MXFP4_G32 ? kFmtMxfp4
-                 : fmt == SVDQ_FMT_W8A8      ? kFmtW8a8
-                 : fmt == SVDQ_FMT_FP8_G128  ? kFmtFp8
-                                             : kFmtInt4;
-  cudaError_t e = launch_prologue(kf, tx, tl1, p,
-                                  static_cast<cudaStream_t>(cuda_stream));
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  const bool fp8 = fmt == SVDQ_FMT_FP8_G128;
+  cudaError_t e;
+  if (fp8 && rank == 0) {
+    e = launch_quantize_fp8(X_bf16, p, stream);
+  } else {
+    // X and L1 seen as [K/64 column blocks][rows][64 columns]: one load brings kProBoxes (FP8: two, one
+    // group) 64-column boxes (128B-swizzled) of 32 (FP8: 128) X rows or of all L1 rows
+    const uint32_t boxes = fp8 ? 2 : kProBoxes;
+    CUtensorMap tx, tl1;
+    const uint64_t rs = static_cast<uint64_t>(K) * 2;
+    if (!make_tmap_3d(&tx, X_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, M, K / 64, rs, 128, 64, fp8 ? 128 : 32, boxes,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+      return SVDQ_ERR_CUDA;
+    if (rank > 0) {
+      if (!make_tmap_3d(&tl1, L1_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, rank, K / 64, rs, 128, 64, rank, boxes,
+                        CU_TENSOR_MAP_SWIZZLE_128B))
+        return SVDQ_ERR_CUDA;
+    } else {
+      tl1 = tx;
+    }
+    const int kf = fmt == SVDQ_FMT_NVFP4_G16   ? kFmtNvfp4
+                   : fmt == SVDQ_FMT_MXFP4_G32 ? kFmtMxfp4
+                   : fmt == SVDQ_FMT_W8A8      ? kFmtW8a8
+                                               : kFmtInt4;
+    e = fp8 ? launch_prologue_fp8(tx, tl1, p, stream) : launch_prologue(kf, tx, tl1, p, stream);
+  }
   if (e != cudaSuccess) return cuda_fail(e);
   t_last_launch_count = 1;
   return SVDQ_OK;

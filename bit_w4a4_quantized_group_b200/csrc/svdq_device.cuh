@@ -13,7 +13,6 @@ constexpr int kFmtNvfp4 = 1;
 constexpr int kFmtInt4 = 2;
 constexpr int kFmtMxfp4 = 3;
 constexpr int kFmtW8a8 = 4;
-constexpr int kFmtFp8 = 5;
 
 // Codes recorded in the device error word when a bounded wait runs out.
 enum : int {
@@ -175,6 +174,9 @@ struct GluParams {
   uint8_t* scales;
   int* err;
 };
+// FP8 prologue with (rank > 0) and without a branch.
+cudaError_t launch_prologue_fp8(const CUtensorMap& tx, const CUtensorMap& tl1, const ProParams& p, cudaStream_t s);
+cudaError_t launch_quantize_fp8(const void* X, const ProParams& p, cudaStream_t s);
 cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s);
 cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s);
 
