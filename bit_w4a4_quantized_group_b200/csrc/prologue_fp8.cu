@@ -7,8 +7,8 @@
 //
 // With a branch.  A CTA owns 128 rows and, in a cluster of up to 8 CTAs that split K, a share of the
 // 128-column groups.  TMA brings a group's X tile (two 128-byte-swizzled boxes of 64 columns) and
-// L1 rows into a ring.  Sixteen warps form X_hat from shared memory: 16 neighbouring lanes hold one
-// group of one row, so that a thread keeps its 8 columns' lambda in registers over all its rows, a
+// L1 rows into a ring.  Sixteen warps, two sets in turn, form X_hat from shared memory: 16 neighbouring
+// lanes hold one group of one row, so that a thread keeps its 8 columns' reciprocals over its rows, a
 // row's codes leave as 128 contiguous bytes, and the group maximum takes four shuffles for two rows
 // at once.  X_hat goes back to the place it came from, where the swizzle makes it the A operand of
 // the tensor core: tcgen05 kind::f16 MMAs (M = 128, N = rank) accumulate Z in TMEM over the CTA's
@@ -18,12 +18,20 @@
 // Without a branch.  Nothing is shared between threads but the group maximum: plain 16-byte loads,
 // the same arithmetic, kRows rows of the same 8 columns per thread.
 //
-// What bounds them: memory in principle (3 bytes per element); the exact divide (five packed FMA-pipe
-// instructions per pair) and the conversions make the instruction issue nearly as busy.
+// What bounds them: memory in principle (3 bytes per element); the conversions and the divide make
+// the instruction issue nearly as busy.
 //
-// The divide x / lambda is the correctly rounded one (Markstein's two corrections, as in prologue.cu,
-// with y = RN(1 / lambda)); the sign of x is put back afterwards, since the corrections lose that of a
-// zero quotient in this order.
+// The divide.  X_hat = bf16(RN_f32(x / lambda)) is formed as bf16(q), q = fma(x, yh, x yl), with
+// yh = RD(1 / lambda) and yl = RN(yh (1 - lambda yh)) (the remainder is exact under FMA): yh + yl is
+// 1 / lambda to 2^-45, so q's value before its rounding is within 2^-44 of the quotient, relatively.
+// That gives the same bf16 always.  A difference would need the quotient that close to a point h where
+// the two-step rounding changes, half an fp32 ulp beside a tie of bf16: h = (M 2^16 +- 1) 2^j with M
+// odd, 257 <= M <= 511.  With the significands a of x (8 bits) and b of lambda (24 bits) as integers,
+// b (M 2^16 +- 1) would have to lie within 2^5 of a multiple of 2^40.  Its low 16 bits are those of
+// +-b, so b = B 2^16 + s with |s| <= 32 and B <= 256; then +-B + s M must vanish modulo 2^16, and
+// |s| M <= 16352 leaves only s M = -+B, which M > B and B >= 128 rule out.  (The quotient
+// must be a normal number well above 2^-126, like the remainder of any such divide.)  yl >= 0 keeps
+// the sign of a zero.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <atomic>
@@ -37,10 +45,14 @@ namespace svdq {
 namespace {
 
 // ------------------------------------------------------------------ arithmetic shared by both kernels
-// The divisors of a thread's 8 columns, as pairs: -lambda and RN(1 / lambda).
+// Reciprocals of a thread's 8 columns in two parts, as pairs.
 struct Divisors {
-  float2 nb[4], y[4];
+  float2 yh[4], yl[4];
 };
+__device__ __forceinline__ float2 reciprocal2(float lam) {      // (yh, yl)
+  const float yh = __frcp_rd(lam);
+  return make_float2(yh, fmaf(-lam, yh, 1.f) * yh);
+}
 // X_hat of 8 elements: four bf16 pairs.
 template <bool LAM>
 __device__ __forceinline__ uint4 smooth8(uint4 v, const Divisors& d) {
@@ -49,20 +61,15 @@ __device__ __forceinline__ uint4 smooth8(uint4 v, const Divisors& d) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 a = make_float2(bf16x2_lo(w[e]), bf16x2_hi(w[e]));
-    float2 q = __fmul2_rn(a, d.y[e]);
-    q = __ffma2_rn(__ffma2_rn(d.nb[e], q, a), d.y[e], q);
-    q = __ffma2_rn(__ffma2_rn(d.nb[e], q, a), d.y[e], q);
+    const float2 q = __ffma2_rn(a, d.yh[e], __fmul2_rn(a, d.yl[e]));
     const __nv_bfloat162 h = __floats2bfloat162_rn(q.x, q.y);
-    w[e] = (*reinterpret_cast<const uint32_t*>(&h) & 0x7FFF7FFFu) | (w[e] & 0x80008000u);
+    w[e] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The scale byte that 8 elements need by themselves (the group's is the largest of its lanes').
 __device__ __forceinline__ uint32_t byte_of8(uint4 v) {
-  auto abs2 = [](uint32_t w) {
-    const uint32_t a = w & 0x7FFF7FFFu;
-    return *reinterpret_cast<const __nv_bfloat162*>(&a);
-  };
+  auto abs2 = [](const uint32_t& w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
   const __nv_bfloat162 m = __hmax2(__hmax2(abs2(v.x), abs2(v.y)), __hmax2(abs2(v.z), abs2(v.w)));
   return fp8_scale_byte(fmaxf(__low2float(m), __high2float(m)));
 }
@@ -110,8 +117,9 @@ __global__ void __launch_bounds__(kQThreads) quantize_fp8_kernel(const __nv_bflo
     const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      d.nb[e] = make_float2(-l[2 * e], -l[2 * e + 1]);
-      d.y[e] = make_float2(__frcp_rn(l[2 * e]), __frcp_rn(l[2 * e + 1]));
+      const float2 r0 = reciprocal2(l[2 * e]), r1 = reciprocal2(l[2 * e + 1]);
+      d.yh[e] = make_float2(r0.x, r1.x);
+      d.yl[e] = make_float2(r0.y, r1.y);
     }
   }
   uint32_t sb[kQRows / 2];
@@ -154,9 +162,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16p(int m, int n) {
 // Padded row of a partial Z tile, in floats: 16 bytes more than the rank spread a column over the banks.
 __host__ __device__ constexpr int zrow(int rank) { return rank + 4; }
 __host__ __device__ constexpr uint32_t pstage_bytes(int rank) { return kXBytes + 256u * rank + kLamBytes; }
-__host__ __device__ constexpr uint32_t red_bytes(int rank) { return (kRowsP + kMaxSplitP - 1) * zrow(rank) * 4; }
+// Partial sums that ks - 1 other CTAs send: [sender][a CTA's share of the rows][zrow].
+__host__ __device__ constexpr uint32_t red_bytes(int rank, int ks) {
+  return static_cast<uint32_t>((ks - 1) * ((kRowsP + ks - 1) / ks) * zrow(rank) * 4);
+}
 __host__ __device__ constexpr uint32_t ptmem_cols(int rank) { return rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
-constexpr int kMaxStagesP = 5;
+constexpr int kMaxStagesP = 4;            // even: a set of compute warps meets only its own slots, each in turn
 
 struct PTail {
   uint64_t full[kMaxStagesP];     // X and L1 tiles (TMA) and the divisors (the producer's lanes) are there
@@ -177,7 +188,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   const int rank = p.rank, S = p.stages, ks = p.ksplit;
   const uint32_t stage = pstage_bytes(rank);
   float* red = reinterpret_cast<float*>(smem + S * stage);
-  PTail* sh = reinterpret_cast<PTail*>(smem + S * stage + (ks > 1 ? red_bytes(rank) : 0));
+  PTail* sh = reinterpret_cast<PTail*>(smem + S * stage + red_bytes(rank, ks));
   volatile int* abort_flag = &sh->abort_flag;
 
   const int warp = threadIdx.x >> 5;
@@ -195,7 +206,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       ptx::mbar_init(&sh->full[s], 32);
-      ptx::mbar_init(&sh->xh_full[s], kComputeWarps);
+      ptx::mbar_init(&sh->xh_full[s], kComputeWarps / 2);
       ptx::mbar_init(&sh->empty[s], 1);
     }
     ptx::mbar_init(&sh->acc_full, 1);
@@ -245,8 +256,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (SVDQ_IN_SMEM(smem_raw, ls + 128 + i * 32 + lane, 4, p.err)) {
-            ls[i * 32 + lane] = l[i];
-            ls[128 + i * 32 + lane] = __frcp_rn(l[i]);
+            const float2 y = reciprocal2(l[i]);
+            ls[i * 32 + lane] = y.x;
+            ls[128 + i * 32 + lane] = y.y;
           }
         }
         if (g + 1 < ng)
@@ -281,61 +293,72 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       if (++s == S) { s = 0; ph ^= 1u; }
     }
   } else {
-    // ------------------------------------------------------------ compute warps: 8 rows of every tile each
+    // ------------------------------------------------------------ compute warps
+    // Two sets of eight warps take the tiles in turn, so that one set's waits and stores overlap the
+    // other's arithmetic; a warp has 16 rows of its set's tile, in two halves.
+    constexpr int kSet = kComputeWarps / 2;
+    const int set = warp / kSet;
     const int c = lane & 15;                               // 16-byte chunk of the 128-column group
-    const int r0 = warp * 8 + (lane >> 4);                 // rows r0, r0 + 2, r0 + 4, r0 + 6
+    const int r0 = (warp % kSet) * 16 + (lane >> 4);       // rows r0, r0 + 2, ...
     uint8_t* scales = static_cast<uint8_t*>(p.scales);
-    int s = 0;
-    uint32_t ph = 0;
-    for (int g = 0; g < ng; ++g) {
+    int s = set % S;
+    uint32_t ph = static_cast<uint32_t>(set / S) & 1u;
+    for (int g = set; g < ng; g += 2) {
       if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteProFull)) break;
       uint8_t* st = smem + s * stage;
       Divisors d;
       if (LAM) {
         const float4* ls = reinterpret_cast<const float4*>(st + kXBytes + 256 * rank) + 2 * c;
-        const float4 l0 = ls[0], l1 = ls[1], y0 = ls[32], y1 = ls[33];
-        d.nb[0] = make_float2(-l0.x, -l0.y);
-        d.nb[1] = make_float2(-l0.z, -l0.w);
-        d.nb[2] = make_float2(-l1.x, -l1.y);
-        d.nb[3] = make_float2(-l1.z, -l1.w);
-        d.y[0] = make_float2(y0.x, y0.y);
-        d.y[1] = make_float2(y0.z, y0.w);
-        d.y[2] = make_float2(y1.x, y1.y);
-        d.y[3] = make_float2(y1.z, y1.w);
-      }
-      uint4 v[4];
-      uint32_t sb[2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 2 * i;
-        uint8_t* at = st + (c >> 3) * (kXBytes / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        if (!SVDQ_IN_SMEM(smem_raw, at, 16, p.err)) at = st;
-        v[i] = smooth8<LAM>(*reinterpret_cast<const uint4*>(at), d);
-        if (LAM) *reinterpret_cast<uint4*>(at) = v[i];
-        const uint32_t b = byte_of8(v[i]);
-        sb[i / 2] = i & 1 ? sb[i / 2] | (b << 16) : b;
-      }
-      // X_hat is in place: hand the stage to the MMA warp before the codes are formed
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh->xh_full[s]);
-#pragma unroll
-      for (int o = 1; o <= 8; o <<= 1) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
+        const float4 h0 = ls[0], h1 = ls[1], l0 = ls[32], l1 = ls[33];
+        d.yh[0] = make_float2(h0.x, h0.y);
+        d.yh[1] = make_float2(h0.z, h0.w);
+        d.yh[2] = make_float2(h1.x, h1.y);
+        d.yh[3] = make_float2(h1.z, h1.w);
+        d.yl[0] = make_float2(l0.x, l0.y);
+        d.yl[1] = make_float2(l0.z, l0.w);
+        d.yl[2] = make_float2(l1.x, l1.y);
+        d.yl[3] = make_float2(l1.z, l1.w);
       }
       const int grp = gb + g;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = m0 + r0 + 2 * i;
-        const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
-        if (row < p.M && SVDQ_IN_GLOBAL(grp < G, p.err))
-          *reinterpret_cast<uint2*>(p.codes + static_cast<size_t>(row) * p.K + grp * 128 + c * 8) = codes8(v[i], b);
-        // rows past M read as zeros and get byte 0
-        if (c == 0) scales[fp8_sf_offset(row, grp, sfb)] = static_cast<uint8_t>(b);
-        if (grp == G - 1 && c > 0 && grp + c < 4 * sfb) scales[fp8_sf_offset(row, grp + c, sfb)] = 0;
+      for (int half = 0; half < 2; ++half) {
+        uint4 v[4];
+        uint32_t sb[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + 8 * half + 2 * i;
+          uint8_t* at = st + (c >> 3) * (kXBytes / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          if (!SVDQ_IN_SMEM(smem_raw, at, 16, p.err)) at = st;
+          v[i] = smooth8<LAM>(*reinterpret_cast<const uint4*>(at), d);
+          if (LAM) *reinterpret_cast<uint4*>(at) = v[i];
+          const uint32_t b = byte_of8(v[i]);
+          sb[i / 2] = i & 1 ? sb[i / 2] | (b << 16) : b;
+        }
+        if (half == 1) {
+          // X_hat is in place: hand the stage to the MMA warp before the last codes are formed
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh->xh_full[s]);
+        }
+#pragma unroll
+        for (int o = 1; o <= 8; o <<= 1) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
+        }
+        uint8_t* dst = p.codes + static_cast<size_t>(m0 + r0 + 8 * half) * p.K + grp * 128 + c * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = m0 + r0 + 8 * half + 2 * i;
+          const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+          if (row < p.M && SVDQ_IN_GLOBAL(grp < G, p.err)) *reinterpret_cast<uint2*>(dst) = codes8(v[i], b);
+          dst += 2 * static_cast<size_t>(p.K);
+          // rows past M read as zeros and get byte 0
+          if (c == 0) scales[fp8_sf_offset(row, grp, sfb)] = static_cast<uint8_t>(b);
+          if (grp == G - 1 && c > 0 && grp + c < 4 * sfb) scales[fp8_sf_offset(row, grp + c, sfb)] = 0;
+        }
       }
-      if (++s == S) { s = 0; ph ^= 1u; }
+      s += 2;                                              // S >= 2
+      if (s >= S) { s -= S; ph ^= 1u; }
     }
     if (warp < 4) {
       // ---------------------------------------------------------- Z: thread = row, column = rank index
@@ -367,7 +390,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           const int rows = min(share, nrow - lane * share);
           if (rows > 0)
             ptx::bulk_copy_to_cta(
-                ptx::mapa_shared(ptx::smem_u32(red + split * share * zrow(rank)), static_cast<uint32_t>(lane)),
+                ptx::mapa_shared(ptx::smem_u32(red + (split - (split > lane ? 1 : 0)) * share * zrow(rank)),
+                                 static_cast<uint32_t>(lane)),
                 part + lane * share * zrow(rank), static_cast<uint32_t>(rows * zrow(rank) * 4),
                 ptx::mapa_shared(ptx::smem_u32(&sh->red_full), static_cast<uint32_t>(lane)));
         }
@@ -392,7 +416,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const int r = i / per, q = i % per * 4;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int x = 0; x < ks; ++x) {
-        const float* src = (x == split ? mine : red + x * share * zrow(rank)) + r * zrow(rank) + q;
+        const float* src = (x == split ? mine : red + (x - (x > split ? 1 : 0)) * share * zrow(rank)) + r * zrow(rank) + q;
         if (!SVDQ_IN_SMEM(smem_raw, src, 16, p.err)) continue;
         const float4 v = *reinterpret_cast<const float4*>(src);
         a.x += v.x;
@@ -414,14 +438,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 }
 
 size_t psmem(int rank, int stages, int ks) {
-  return 1024 + static_cast<size_t>(stages) * pstage_bytes(rank) + (ks > 1 ? red_bytes(rank) : 0) + sizeof(PTail);
+  return 1024 + static_cast<size_t>(stages) * pstage_bytes(rank) + red_bytes(rank, ks) + sizeof(PTail);
 }
-// Stages that fit next to the partial sums; the ring also holds a CTA's own partial tile.
-int pstages(int rank, int ks) {
-  int s = kMaxStagesP;
-  while (s > 2 && psmem(rank, s, ks) > 232448) --s;
-  return s;
-}
+// Four stages where they fit next to the partial sums (ranks up to 64), else two; the ring also holds
+// a CTA's own partial tile.
+int pstages(int rank, int ks) { return psmem(rank, kMaxStagesP, ks) <= 232448 ? kMaxStagesP : 2; }
+static_assert(1024 + 2 * pstage_bytes(128) + red_bytes(128, kMaxSplitP) + sizeof(PTail) <= 232448, "two stages always fit");
+static_assert(kRowsP * zrow(128) * 4 <= 2 * pstage_bytes(128) && kRowsP * zrow(16) * 4 <= 2 * pstage_bytes(16),
+              "a partial Z tile in the ring");
 
 template <bool LAM>
 void fill_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int blocks, int ks, size_t smem,
