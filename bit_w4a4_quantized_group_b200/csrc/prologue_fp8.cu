@@ -5,7 +5,7 @@
 //
 // The data flow is that of "SVDQuant 阅读笔记" §6.1 "算法 2" steps 1-3.  Two kernels:
 //
-// With a branch.  A CTA owns 128 rows and, in a cluster of up to 8 CTAs that split K, a share of the
+// With a branch.  A CTA owns 128 or 64 rows and, in a cluster of up to 8 CTAs that split K, a share of the
 // 128-column groups.  TMA brings a group's X tile (two 128-byte-swizzled boxes of 64 columns) and
 // L1 rows into a ring.  Sixteen warps, two sets in turn, form X_hat from shared memory: 16 neighbouring
 // lanes hold one group of one row, so that a thread keeps its 8 columns' reciprocals over its rows, a
@@ -147,11 +147,12 @@ __global__ void __launch_bounds__(kQThreads) quantize_fp8_kernel(const __nv_bflo
 }
 
 // ------------------------------------------------------------------ with a branch
-constexpr int kRowsP = 128;
 constexpr int kComputeWarps = 16;
 constexpr int kProdWarp = kComputeWarps, kMmaWarp = kComputeWarps + 1;
 constexpr int kThreadsP = 32 * (kComputeWarps + 2);
-constexpr uint32_t kXBytes = kRowsP * 256;              // two boxes of 128 rows x 64 bf16
+constexpr int kMmaRows = 128;                           // rows of an MMA, see prologue_fp8_kernel
+// An X tile of `rows` rows: two boxes of rows x 64 bf16.
+__host__ __device__ constexpr uint32_t x_bytes(int rows) { return rows * 256u; }
 constexpr uint32_t kLamBytes = 1024;                    // lambda and RN(1 / lambda) of 128 columns
 constexpr int kMaxSplitP = 8;
 
@@ -161,10 +162,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16p(int m, int n) {
 }
 // Padded row of a partial Z tile, in floats: 16 bytes more than the rank spread a column over the banks.
 __host__ __device__ constexpr int zrow(int rank) { return rank + 4; }
-__host__ __device__ constexpr uint32_t pstage_bytes(int rank) { return kXBytes + 256u * rank + kLamBytes; }
+__host__ __device__ constexpr uint32_t pstage_bytes(int rows, int rank) {
+  return x_bytes(rows) + 256u * rank + kLamBytes;
+}
 // Partial sums that ks - 1 other CTAs send: [sender][a CTA's share of the rows][zrow].
-__host__ __device__ constexpr uint32_t red_bytes(int rank, int ks) {
-  return static_cast<uint32_t>((ks - 1) * ((kRowsP + ks - 1) / ks) * zrow(rank) * 4);
+__host__ __device__ constexpr uint32_t red_bytes(int rows, int rank, int ks) {
+  return static_cast<uint32_t>((ks - 1) * ((rows + ks - 1) / ks) * zrow(rank) * 4);
 }
 __host__ __device__ constexpr uint32_t ptmem_cols(int rank) { return rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 constexpr int kMaxStagesP = 4;            // even: a set of compute warps meets only its own slots, each in turn
@@ -179,26 +182,30 @@ struct PTail {
   int abort_flag;
 };
 
-template <bool LAM>
+// R rows per CTA, 128 or 64.  The MMAs have 128 rows either way: with R = 64 the upper half of the A
+// tile is whatever follows in shared memory (the next box, L1, the next stage; slack behind the last)
+// and the accumulator's upper lanes are not read.
+template <bool LAM, int R>
 __global__ void __launch_bounds__(kThreadsP, 1)
     prologue_fp8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_l1,
                         ProParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int rank = p.rank, S = p.stages, ks = p.ksplit;
-  const uint32_t stage = pstage_bytes(rank);
+  constexpr uint32_t kXBytes = x_bytes(R);
+  const uint32_t stage = pstage_bytes(R, rank);
   float* red = reinterpret_cast<float*>(smem + S * stage);
-  PTail* sh = reinterpret_cast<PTail*>(smem + S * stage + red_bytes(rank, ks));
+  PTail* sh = reinterpret_cast<PTail*>(smem + S * stage + red_bytes(R, rank, ks));
   volatile int* abort_flag = &sh->abort_flag;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int split = static_cast<int>(blockIdx.x) % ks;
-  const int m0 = static_cast<int>(blockIdx.x) / ks * kRowsP;
+  const int m0 = static_cast<int>(blockIdx.x) / ks * R;
   const int G = p.K >> 7, sfb = (p.K + 511) >> 9;
   const int gb = static_cast<int>(static_cast<int64_t>(G) * split / ks);                 // this CTA's groups
   const int ng = static_cast<int>(static_cast<int64_t>(G) * (split + 1) / ks) - gb;      // >= 1: ks <= G
-  const int nrow = min(kRowsP, p.M - m0);
+  const int nrow = min(R, p.M - m0);
   // K split: CTA r adds up the Z rows [r share, r share + own) of the block
   const int share = (nrow + ks - 1) / ks;
   const int own = max(0, min(share, nrow - split * share));
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     // ------------------------------------------------------------ Z += X_hat L1^T
     int s = 0;
     uint32_t ph = 0;
-    const uint32_t idesc = idesc_bf16p(kRowsP, rank);
+    const uint32_t idesc = idesc_bf16p(kMmaRows, rank);
     const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem));
     for (int g = 0; g < ng; ++g) {
       if (!wait_bounded(&sh->xh_full[s], ph, abort_flag, p.err, kErrSiteProPair)) break;
@@ -295,11 +302,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   } else {
     // ------------------------------------------------------------ compute warps
     // Two sets of eight warps take the tiles in turn, so that one set's waits and stores overlap the
-    // other's arithmetic; a warp has 16 rows of its set's tile, in two halves.
+    // other's arithmetic; a warp has an eighth of its set's tile's rows.
     constexpr int kSet = kComputeWarps / 2;
     const int set = warp / kSet;
     const int c = lane & 15;                               // 16-byte chunk of the 128-column group
-    const int r0 = (warp % kSet) * 16 + (lane >> 4);       // rows r0, r0 + 2, ...
+    const int r0 = (warp % kSet) * (R / kSet) + (lane >> 4);       // rows r0, r0 + 2, ...
     uint8_t* scales = static_cast<uint8_t*>(p.scales);
     int s = set % S;
     uint32_t ph = static_cast<uint32_t>(set / S) & 1u;
@@ -320,42 +327,42 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         d.yl[3] = make_float2(l1.z, l1.w);
       }
       const int grp = gb + g;
+      constexpr int kR = R / (2 * kSet);                   // rows of a thread
+      uint4 v[kR];
+      uint8_t* at0 = st + (c >> 3) * (kXBytes / 2) + r0 * 128;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint4 v[4];
-        uint32_t sb[2];
+      for (int i = 0; i < kR; ++i) {
+        uint8_t* at = at0 + i * 256 + (((c & 7) ^ ((r0 + 2 * i) & 7)) << 4);
+        v[i] = SVDQ_IN_SMEM(smem_raw, at, 16, p.err) ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+      }
+      uint32_t sb[kR / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + 8 * half + 2 * i;
-          uint8_t* at = st + (c >> 3) * (kXBytes / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          if (!SVDQ_IN_SMEM(smem_raw, at, 16, p.err)) at = st;
-          v[i] = smooth8<LAM>(*reinterpret_cast<const uint4*>(at), d);
-          if (LAM) *reinterpret_cast<uint4*>(at) = v[i];
-          const uint32_t b = byte_of8(v[i]);
-          sb[i / 2] = i & 1 ? sb[i / 2] | (b << 16) : b;
-        }
-        if (half == 1) {
-          // X_hat is in place: hand the stage to the MMA warp before the last codes are formed
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sh->xh_full[s]);
-        }
+      for (int i = 0; i < kR; ++i) {
+        uint8_t* at = at0 + i * 256 + (((c & 7) ^ ((r0 + 2 * i) & 7)) << 4);
+        v[i] = smooth8<LAM>(v[i], d);
+        if (LAM && SVDQ_IN_SMEM(smem_raw, at, 16, p.err)) *reinterpret_cast<uint4*>(at) = v[i];
+        const uint32_t b = byte_of8(v[i]);
+        sb[i / 2] = i & 1 ? sb[i / 2] | (b << 16) : b;
+      }
+      // X_hat is in place: hand the stage to the MMA warp before the codes are formed
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh->xh_full[s]);
 #pragma unroll
-        for (int o = 1; o <= 8; o <<= 1) {
+      for (int o = 1; o <= 8; o <<= 1) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
-        }
-        uint8_t* dst = p.codes + static_cast<size_t>(m0 + r0 + 8 * half) * p.K + grp * 128 + c * 8;
+        for (int i = 0; i < kR / 2; ++i) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
+      }
+      uint8_t* dst = p.codes + static_cast<size_t>(m0 + r0) * p.K + grp * 128 + c * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = m0 + r0 + 8 * half + 2 * i;
-          const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
-          if (row < p.M && SVDQ_IN_GLOBAL(grp < G, p.err)) *reinterpret_cast<uint2*>(dst) = codes8(v[i], b);
-          dst += 2 * static_cast<size_t>(p.K);
-          // rows past M read as zeros and get byte 0
-          if (c == 0) scales[fp8_sf_offset(row, grp, sfb)] = static_cast<uint8_t>(b);
-          if (grp == G - 1 && c > 0 && grp + c < 4 * sfb) scales[fp8_sf_offset(row, grp + c, sfb)] = 0;
-        }
+      for (int i = 0; i < kR; ++i) {
+        const int row = m0 + r0 + 2 * i;
+        const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+        if (row < p.M && SVDQ_IN_GLOBAL(grp < G, p.err)) *reinterpret_cast<uint2*>(dst) = codes8(v[i], b);
+        dst += 2 * static_cast<size_t>(p.K);
+        // rows past M read as zeros and get byte 0
+        if (c == 0) scales[fp8_sf_offset(row, grp, sfb)] = static_cast<uint8_t>(b);
+        if (grp == G - 1 && c > 0 && grp + c < 4 * sfb) scales[fp8_sf_offset(row, grp + c, sfb)] = 0;
       }
       s += 2;                                              // S >= 2
       if (s >= S) { s -= S; ph ^= 1u; }
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const int row = warp * 32 + lane;
         const uint32_t base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll 1
-        for (int q = 0; q < rank; q += 16) {
+        for (int q = 0; q < (row < R ? rank : 0); q += 16) {       // the same for a warp
           uint32_t z[16];
           ptx::tmem_ld_32x32b_x16(base + q, z);
           ptx::tmem_wait_ld();
@@ -437,17 +444,22 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   }
 }
 
-size_t psmem(int rank, int stages, int ks) {
-  return 1024 + static_cast<size_t>(stages) * pstage_bytes(rank) + red_bytes(rank, ks) + sizeof(PTail);
+size_t psmem(int rows, int rank, int stages, int ks) {
+  // the slack lets the unused half of the last stage's A tile be read
+  return 1024 + static_cast<size_t>(stages) * pstage_bytes(rows, rank) + red_bytes(rows, rank, ks) + sizeof(PTail) +
+         (rows < kMmaRows ? x_bytes(kMmaRows) - x_bytes(rows) : 0);
 }
-// Four stages where they fit next to the partial sums (ranks up to 64), else two; the ring also holds
-// a CTA's own partial tile.
-int pstages(int rank, int ks) { return psmem(rank, kMaxStagesP, ks) <= 232448 ? kMaxStagesP : 2; }
-static_assert(1024 + 2 * pstage_bytes(128) + red_bytes(128, kMaxSplitP) + sizeof(PTail) <= 232448, "two stages always fit");
-static_assert(kRowsP * zrow(128) * 4 <= 2 * pstage_bytes(128) && kRowsP * zrow(16) * 4 <= 2 * pstage_bytes(16),
+constexpr size_t kSmemMax = 232448;
+// Four stages where they fit next to the partial sums (128 rows: ranks up to 64), else two; the ring
+// also holds a CTA's own partial tile.
+int pstages(int rows, int rank, int ks) { return psmem(rows, rank, kMaxStagesP, ks) <= kSmemMax ? kMaxStagesP : 2; }
+static_assert(1024 + 2 * pstage_bytes(128, 128) + red_bytes(128, 128, kMaxSplitP) + sizeof(PTail) <= kSmemMax,
+              "two stages always fit");
+static_assert(128 * zrow(128) * 4 <= 2 * pstage_bytes(128, 128) && 64 * zrow(128) * 4 <= 2 * pstage_bytes(64, 128) &&
+                  128 * zrow(16) * 4 <= 2 * pstage_bytes(128, 16) && 64 * zrow(16) * 4 <= 2 * pstage_bytes(64, 16),
               "a partial Z tile in the ring");
 
-template <bool LAM>
+template <bool LAM, int R>
 void fill_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int blocks, int ks, size_t smem,
                  cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(blocks) * static_cast<unsigned>(ks), 1, 1);
@@ -465,7 +477,6 @@ void fill_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int bl
 }
 
 // Clusters of ks CTAs that the current device holds at once (0 on error), asked once per device.
-template <bool LAM>
 int resident_clusters(int ks) {
   static std::atomic<int> cache[64][kMaxSplitP + 1];     // 0: not asked yet, else 1 + the figure
   int dev = 0;
@@ -474,10 +485,11 @@ int resident_clusters(int ks) {
   if (known > 0) return known - 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  fill_config<LAM>(cfg, attr, 1, ks, 232448, nullptr);
+  fill_config<true, 128>(cfg, attr, 1, ks, kSmemMax, nullptr);
   cfg.numAttrs = 1;                                      // the cluster alone
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, prologue_fp8_kernel<LAM>, &cfg) != cudaSuccess) {
+  if (set_smem_limit_once(reinterpret_cast<const void*>(prologue_fp8_kernel<true, 128>), kSmemMax) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, prologue_fp8_kernel<true, 128>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -485,31 +497,51 @@ int resident_clusters(int ks) {
   return n;
 }
 
-template <bool LAM>
+template <bool LAM, int R>
 cudaError_t launch_branch(const CUtensorMap& tx, const CUtensorMap& tl1, ProParams p, cudaStream_t s) {
-  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(prologue_fp8_kernel<LAM>), 232448);
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(prologue_fp8_kernel<LAM, R>), kSmemMax);
   if (e != cudaSuccess) return e;
-  const int blocks = p.Mpad / kRowsP, G = p.K / 128;
-  // the widest K split with every cluster resident at once
-  p.ksplit = 1;
-  for (int ks = G < kMaxSplitP ? G : kMaxSplitP; ks > 1; --ks)
-    if (resident_clusters<LAM>(ks) >= blocks) {
-      p.ksplit = ks;
-      break;
-    }
-  p.stages = pstages(p.rank, p.ksplit);
+  p.stages = pstages(R, p.rank, p.ksplit);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  fill_config<LAM>(cfg, attr, blocks, p.ksplit, psmem(p.rank, p.stages, p.ksplit), s);
-  e = cudaLaunchKernelEx(&cfg, prologue_fp8_kernel<LAM>, tx, tl1, p);
+  fill_config<LAM, R>(cfg, attr, p.Mpad / R, p.ksplit, psmem(R, p.rank, p.stages, p.ksplit), s);
+  e = cudaLaunchKernelEx(&cfg, prologue_fp8_kernel<LAM, R>, tx, tl1, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_prologue_fp8(const CUtensorMap& tx, const CUtensorMap& tl1, const ProParams& p, cudaStream_t s) {
-  return p.lam ? launch_branch<true>(tx, tl1, p, s) : launch_branch<false>(tx, tl1, p, s);
+int prologue_fp8_rows(int M, int K, int num_sms, int* ksplit) {
+  // 128 or 64 rows per CTA and the widest K split with every cluster resident at once: the least time
+  // by rows x groups of a CTA x waves (4608 x 3072, rank 32: 36 blocks of 128 rows split by 3 leave
+  // 40 of 148 SMs idle, 72 of 64 rows split by 2 leave 4).
+  const int G = K / 128;
+  int64_t best = 0;
+  int rows = 0;
+  for (int r : {128, 64}) {
+    const int64_t blocks = (static_cast<int64_t>(M) + 127) / 128 * (128 / r);
+    int ks = 1;
+    for (int k = G < kMaxSplitP ? G : kMaxSplitP; k > 1; --k)
+      if (resident_clusters(k) >= blocks) {
+        ks = k;
+        break;
+      }
+    const int64_t waves = ks > 1 ? 1 : (blocks + num_sms - 1) / num_sms;
+    const int64_t cost = waves * r * ((G + ks - 1) / ks);
+    if (rows == 0 || cost < best) {
+      best = cost;
+      rows = r;
+      *ksplit = ks;
+    }
+  }
+  return rows;
+}
+
+cudaError_t launch_prologue_fp8(int rows, const CUtensorMap& tx, const CUtensorMap& tl1, const ProParams& p,
+                                cudaStream_t s) {
+  if (rows == 128) return p.lam ? launch_branch<true, 128>(tx, tl1, p, s) : launch_branch<false, 128>(tx, tl1, p, s);
+  return p.lam ? launch_branch<true, 64>(tx, tl1, p, s) : launch_branch<false, 64>(tx, tl1, p, s);
 }
 
 cudaError_t launch_quantize_fp8(const void* X, const ProParams& p, cudaStream_t s) {

@@ -252,11 +252,13 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
     e = launch_quantize_fp8(X_bf16, p, stream);
   } else {
     // X and L1 seen as [K/64 column blocks][rows][64 columns]: one load brings kProBoxes (FP8: two, one
-    // group) 64-column boxes (128B-swizzled) of 32 (FP8: 128) X rows or of all L1 rows
+    // group) 64-column boxes (128B-swizzled) of 32 (FP8: 128 or 64) X rows or of all L1 rows
     const uint32_t boxes = fp8 ? 2 : kProBoxes;
+    const int rows = fp8 ? prologue_fp8_rows(p.M, p.K, device_sm_count(), &p.ksplit) : 32;
+    if (rows <= 0) return SVDQ_ERR_CUDA;
     CUtensorMap tx, tl1;
     const uint64_t rs = static_cast<uint64_t>(K) * 2;
-    if (!make_tmap_3d(&tx, X_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, M, K / 64, rs, 128, 64, fp8 ? 128 : 32, boxes,
+    if (!make_tmap_3d(&tx, X_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, M, K / 64, rs, 128, 64, rows, boxes,
                       CU_TENSOR_MAP_SWIZZLE_128B))
       return SVDQ_ERR_CUDA;
     if (rank > 0) {
@@ -270,7 +272,7 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
                    : fmt == SVDQ_FMT_MXFP4_G32 ? kFmtMxfp4
                    : fmt == SVDQ_FMT_W8A8      ? kFmtW8a8
                                                : kFmtInt4;
-    e = fp8 ? launch_prologue_fp8(tx, tl1, p, stream) : launch_prologue(kf, tx, tl1, p, stream);
+    e = fp8 ? launch_prologue_fp8(rows, tx, tl1, p, stream) : launch_prologue(kf, tx, tl1, p, stream);
   }
   if (e != cudaSuccess) return cuda_fail(e);
   t_last_launch_count = 1;

@@ -174,8 +174,10 @@ struct GluParams {
   uint8_t* scales;
   int* err;
 };
-// FP8 prologue with (rank > 0) and without a branch.
-cudaError_t launch_prologue_fp8(const CUtensorMap& tx, const CUtensorMap& tl1, const ProParams& p, cudaStream_t s);
+// FP8 prologue with (rank > 0) and without a branch; prologue_fp8_rows picks the rows of a CTA (128 or
+// 64, the box height of tx) and p.ksplit.
+int prologue_fp8_rows(int M, int K, int num_sms, int* ksplit);
+cudaError_t launch_prologue_fp8(int rows, const CUtensorMap& tx, const CUtensorMap& tl1, const ProParams& p, cudaStream_t s);
 cudaError_t launch_quantize_fp8(const void* X, const ProParams& p, cudaStream_t s);
 cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s);
 cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s);
