@@ -1,4 +1,4 @@
-"""ctypes binding of libsvdq (argument marshalling only).
+"""Binding of libsvdq (argument marshalling only): ctypes, and a small CPython extension for the hot calls.
 
 Every function keeps the name of the C entry point in ``include/svdq.h``.
 The ``*_t`` helpers take torch tensors and pass their data pointers and the
@@ -12,6 +12,7 @@ import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libsvdq.so")
+CALLS_PATH = os.path.join(_PKG, "_lib", "svdq_call.so")
 
 SVDQ_OK, SVDQ_ERR_INVALID_ARG, SVDQ_ERR_UNSUPPORTED, SVDQ_ERR_CUDA, SVDQ_ERR_TIMEOUT = range(5)
 SVDQ_FMT_NVFP4_G16 = 1
@@ -44,11 +45,12 @@ class SvdqError(RuntimeError):
 
 
 _lib = None
+_calls = None     # what makes the hot calls, see _bind_calls
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libsvdq.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _calls
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -74,7 +76,30 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         if name not in ("svdq_status_string", "svdq_last_cuda_error"):
             getattr(lib, name).restype = c_int
     _lib = lib
+    _calls = _bind_calls(lib)
     return lib
+
+
+def _bind_calls(lib):
+    """The four hot entry points (prologue, GEMM and the two row operators): through the extension
+    svdq_call, which converts their arguments ten times as fast as ctypes, or, where that was not
+    built, through ctypes.  The same functions with the same positional arguments either way."""
+    if not os.path.exists(CALLS_PATH):
+        return lib
+    from importlib.machinery import ExtensionFileLoader
+    from importlib.util import module_from_spec, spec_from_loader
+    loader = ExtensionFileLoader("svdq_call", CALLS_PATH)
+    mod = module_from_spec(spec_from_loader("svdq_call", loader))
+    loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+               ("svdq_quantize_act_lowrank_down", "svdq_w4a4_gemm_lowrank_up", "svdq_rmsnorm_quantize_act",
+                "svdq_glu_quantize_act")))
+    return mod
+
+
+def _hot():
+    load()
+    return _calls
 
 
 def status_name(status: int) -> str:
@@ -188,7 +213,7 @@ def quantize_act_lowrank_down_t(fmt, X, lam, act_gscale, L1, a_codes, a_scales, 
     """Device prologue on torch tensors (X [M, K] bf16, L1 [r, K] bf16 viewed as any 2-byte dtype).
     `stream` is a raw cudaStream_t handle; None means torch's current stream."""
     M, K = X.shape
-    st = (_lib or load()).svdq_quantize_act_lowrank_down(
+    st = (_calls or _hot()).svdq_quantize_act_lowrank_down(
         _fmt(fmt), M, K, 0 if L1 is None else L1.shape[0], X.data_ptr(), None if lam is None else lam.data_ptr(),
         act_gscale, None if L1 is None else L1.data_ptr(), a_codes.data_ptr(), a_scales.data_ptr(),
         None if Z is None else Z.data_ptr(), _stream() if stream is None else stream)
@@ -198,7 +223,7 @@ def quantize_act_lowrank_down_t(fmt, X, lam, act_gscale, L1, a_codes, a_scales, 
 
 def w4a4_gemm_lowrank_up_t(fmt, M, N, K, rank, a_codes, a_scales, act_gscale, w_codes, w_scales, w_gscale,
                            Z, L2, bias, Y, stream=None):
-    st = (_lib or load()).svdq_w4a4_gemm_lowrank_up(
+    st = (_calls or _hot()).svdq_w4a4_gemm_lowrank_up(
         _fmt(fmt), M, N, K, rank, a_codes.data_ptr(), a_scales.data_ptr(), act_gscale, w_codes.data_ptr(),
         w_scales.data_ptr(), w_gscale, None if Z is None else Z.data_ptr(), None if L2 is None else L2.data_ptr(),
         None if bias is None else bias.data_ptr(), Y.data_ptr(), _stream() if stream is None else stream)
@@ -230,11 +255,21 @@ def _column_vector(t, K, dev, name):
     """Pointer of an fp32 [K] vector (gamma, lambda) on that device; None for None."""
     if t is None:
         return None
-    if t.element_size() != 4 or not t.is_floating_point() or t.shape != (K,) or t.get_device() != dev or \
-            not t.is_contiguous():
+    if t.dtype is not (_f32 or _float32()) or t.numel() != K or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous float32 [{K}] on device {dev}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
     return t.data_ptr()
+
+
+_f32 = None
+
+
+def _float32():
+    global _f32
+    if _f32 is None:
+        import torch
+        _f32 = torch.float32
+    return _f32
 
 
 def _first_matrix(t, name):
@@ -259,7 +294,7 @@ def rmsnorm_quantize_act_t(fmt, X, residual, gamma, eps, H, a_codes, a_scales, s
         ldh, h = _row_ld(H, shape, dtype, dev, "H"), H.data_ptr()
     if dev < 0 or dev != _current_device():
         raise ValueError(f"expected tensors on the current CUDA device, got one on {X.device}")
-    st = (_lib or load()).svdq_rmsnorm_quantize_act(
+    st = (_calls or _hot()).svdq_rmsnorm_quantize_act(
         _fmt(fmt), shape[0], shape[1], X.data_ptr(), ldx, r, ldr, _column_vector(gamma, shape[1], dev, "gamma"), eps,
         h, ldh, a_codes.data_ptr(), a_scales.data_ptr(), _stream() if stream is None else stream)
     if st != SVDQ_OK:
@@ -276,7 +311,7 @@ def glu_quantize_act_t(fmt, act, gate, up, lam, a_codes, a_scales, stream=None):
         ldu, u = _row_ld(up, shape, dtype, dev, "up"), up.data_ptr()
     if dev < 0 or dev != _current_device():
         raise ValueError(f"expected tensors on the current CUDA device, got one on {gate.device}")
-    st = (_lib or load()).svdq_glu_quantize_act(
+    st = (_calls or _hot()).svdq_glu_quantize_act(
         _fmt(fmt), code, shape[0], shape[1], gate.data_ptr(), ldg, u, ldu,
         _column_vector(lam, shape[1], dev, "lam"), a_codes.data_ptr(), a_scales.data_ptr(), _stream() if stream is None else stream)
     if st != SVDQ_OK:

@@ -4,7 +4,7 @@
 
 Each source under ``csrc/`` is compiled to an object in ``_build/`` (in
 parallel), then linked into ``_lib/libsvdq.so`` with the CUDA runtime linked
-statically.  No GPU is needed to build.
+statically.  ``csrc/svdq_call.c`` becomes ``_lib/svdq_call.so``, the binding's CPython extension.  No GPU is needed to build.
 
 ``--debug`` builds ``_lib/libsvdq_debug.so`` instead (objects in ``_build_debug/``):
 the same kernels compiled with -DSVDQ_DEBUG, in which every plain global or
@@ -19,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +28,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libsvdq.so")
+CALLS = os.path.join(LIBDIR, "svdq_call.so")      # CPython extension of the binding, see csrc/svdq_call.c
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(LIBDIR, "libsvdq_debug.so")
 
@@ -74,14 +76,37 @@ def _compile(src: str, verbose: bool, debug: bool = False) -> str:
     return obj
 
 
+def _python_include() -> str:
+    """Directory of Python.h, or "" where Python's headers are not installed."""
+    inc = sysconfig.get_paths()["include"]
+    return inc if os.path.exists(os.path.join(inc, "Python.h")) else ""
+
+
+def _build_calls() -> None:
+    """The binding's extension.  Without Python's headers the binding goes through ctypes alone."""
+    inc = _python_include()
+    if not inc:
+        return
+    tmp = CALLS + ".tmp"
+    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", inc, "-I", INCLUDE,
+           os.path.join(CSRC, "svdq_call.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for svdq_call.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile every CUDA / C++ source of the library for sm_100a; return the .so path
     (the bounds-checking debug library when debug is true)."""
     lib = LIB_DEBUG if debug else LIB
-    if (not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime()):
+    if (not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime()
+            and (debug or os.path.exists(CALLS) or not _python_include())):
         return lib
     os.makedirs(BUILD_DEBUG if debug else BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
+    if not debug:
+        _build_calls()
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose, debug), srcs))

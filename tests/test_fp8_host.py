@@ -178,3 +178,30 @@ def test_layer_refuses_to_be_fed_where_it_cannot():
         lin.forward_normed(X, None, None)
     g = torch.from_numpy(rng.uniform(0.5, 2, 256)).to(torch.bfloat16)
     assert torch.equal(lin.fold_gamma(g), g.float() / torch.from_numpy(lam))
+
+
+def test_hot_calls_convert_arguments_like_ctypes():
+    """The extension behind the helpers gives every entry point the arguments that ctypes gives it: the
+    same refusal for the same bad argument, position by position, and no call on a wrong type."""
+    if B._hot() is B.load():
+        pytest.skip("built without Python's headers")
+    good = {
+        "svdq_quantize_act_lowrank_down": [5, 4, 256, 16, _P, _P, 1.0, _P, _P, _P, _P, None],
+        "svdq_w4a4_gemm_lowrank_up": [5, 4, 128, 256, 16, _P, _P, 1.0, _P, _P, 1.0, _P, _P, _P, _P, None],
+        "svdq_rmsnorm_quantize_act": [5, 4, 256, _P, 256, _P, 256, _P, 1e-6, 2 * _P, 256, _P, _P, None],
+        "svdq_glu_quantize_act": [5, 1, 4, 256, _P, 256, _P, 256, _P, _P, _P, None],
+    }
+    refused = 0
+    for name, args in good.items():
+        fast, plain = getattr(B._hot(), name), getattr(B.load(), name)
+        for i, v in enumerate(args[:-1]):
+            bad = args[:]
+            bad[i] = (-1.0 if name == "svdq_rmsnorm_quantize_act" else 3.0) if isinstance(v, float) else v + 4 if v == _P or v == 2 * _P else -3
+            a, b = fast(*bad), plain(*bad)
+            assert a == b == B.SVDQ_ERR_INVALID_ARG, (name, i, a, b)
+            refused += 1
+            with pytest.raises(TypeError):
+                fast(*(args[:i] + ["x"] + args[i + 1:]))
+        with pytest.raises(TypeError):
+            fast(*args[:-1])
+    assert refused == 50
