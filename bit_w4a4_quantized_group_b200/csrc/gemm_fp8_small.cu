@@ -128,6 +128,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::griddep_launch_dependents();
   // the set-up above may overlap the end of the kernel that writes X and Z
   ptx::griddep_wait();
+  // this thread's four columns of the bias, on their way while the weights stream
+  const int col = 4 * lane;
+  uint2 braw = make_uint2(0u, 0u);
+  if (p.bias) braw = __ldg(reinterpret_cast<const uint2*>(p.bias + n0 + col));
 
   // step k < nk of this CTA is the weights' K step kb + k; its first step, and each one that is a
   // multiple of four, starts a scale block
@@ -140,9 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, b = 0;
       uint32_t ph = 1, sfph = 1;
       for (int k = 0; k < nk + nk_lr; ++k) {
-        if (!wait_bounded(&sh->empty[s], ph, abort_flag, p.err, kErrSiteGemmEmpty)) break;
+        if (!wait_bounded_call(&sh->empty[s], ph, abort_flag, p.err, kErrSiteGemmEmpty)) break;
         if (starts_block(k)) {
-          if (!wait_bounded(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree)) break;
+          if (!wait_bounded_call(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree)) break;
           uint8_t* sf = sf_smem + b * 2 * kSfBlk;
           ptx::mbar_arrive_expect_tx(&sh->sf_full[b], 2 * kSfBlk);
           ptx::tma_load_3d(sf, &tmap_sfw, &sh->sf_full[b], 0, (kb + k) >> 2, n0 >> 7);
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sfdesc0 = ptx::sdesc_sf(ptx::smem_u32(sf_smem));
     const int blocks = ((kb + nk - 1) >> 2) - (kb >> 2) + 1;
     for (int i = 0; i < blocks; ++i) {
-      if (!wait_bounded(&sh->sf_full[b], sfph, abort_flag, p.err, kErrSiteGemmFull)) break;
+      if (!wait_bounded_call(&sh->sf_full[b], sfph, abort_flag, p.err, kErrSiteGemmFull)) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         const uint64_t sd = sfdesc0 + static_cast<uint64_t>(b) * (2 * kSfBlk / 16);
@@ -188,10 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem));
     const uint32_t sfx_skip = static_cast<uint32_t>(m0 & 127) / 32;    // T = 16 has m0 = 0
     for (int k = 0; k < nk + nk_lr; ++k) {
-      if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) break;
+      if (!wait_bounded_call(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) break;
       const bool main_step = k < nk;
       const uint32_t id = static_cast<uint32_t>((kb + k) & 3);
-      if (starts_block(k) && !wait_bounded(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) break;
+      if (starts_block(k) && !wait_bounded_call(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) break;
       ptx::tc_fence_after();
       const bool sf_done = main_step && (id == 3 || k == nk - 1);
       if (ptx::elect_one()) {
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     const int n = q * 32 + lane;
     if (ks > 1) ptx::cluster_wait();
-    if (wait_bounded(&sh->acc_full, 0u, abort_flag, p.err, kErrSiteGemmAccFull)) {
+    if (wait_bounded_call(&sh->acc_full, 0u, abort_flag, p.err, kErrSiteGemmAccFull)) {
       ptx::tc_fence_after();
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
       float* part = reinterpret_cast<float*>(smem) + n;       // [token][128], in the drained ring
@@ -262,25 +266,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();                                           // this CTA's own rows lie in its ring
   bool ok = *abort_flag == 0;
   if (ks > 1) {
-    ok = wait_bounded(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
+    ok = wait_bounded_call(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
     // what the others sent has arrived; when all CTAs say so, every copy has left its source
     __syncwarp();
     ptx::cluster_arrive();
   }
   // The partial sums are added in CTA order; a warp takes a token, a thread four columns.
   if (ok) {
-    const int col = 4 * (threadIdx.x & 31);
-    float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.bias) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.bias + n0 + col));
-      b = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                      __uint_as_float(w.y & 0xFFFF0000u));
-    }
+    const float4 b = make_float4(__uint_as_float(braw.x << 16), __uint_as_float(braw.x & 0xFFFF0000u),
+                                 __uint_as_float(braw.y << 16), __uint_as_float(braw.y & 0xFFFF0000u));
     const float* mine = reinterpret_cast<const float*>(smem) + split * share * kRowsW + col;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = warp; i < own; i += kThreads / 32) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 1
       for (int r = 0; r < ks; ++r) {
         const float* src = r == split ? mine + i * kRowsW : red + (r * share + i) * kRowsW + col;
         if (!SVDQ_IN_SMEM(smem_raw, src, 16, p.err)) continue;

@@ -90,6 +90,17 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
   }
 }
 
+// wait_bounded with its loop out of line, for kernels that run once through their code in a few
+// microseconds: there the time goes into fetching instructions, and the loop is inlined at no site.
+static __device__ __noinline__ bool wait_bounded_loop(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                      int site) {
+  return wait_bounded(bar, parity, abort_flag, err, site);
+}
+__device__ __forceinline__ bool wait_bounded_call(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                  int site) {
+  return ptx::mbar_try_wait(ptx::smem_u32(bar), parity) || wait_bounded_loop(bar, parity, abort_flag, err, site);
+}
+
 // Tile schedule of the persistent pair GEMMs: cluster c takes the contiguous run
 // [begin, begin + count) of the N-fastest tile numbering, so consecutive tiles of a
 // cluster share the M block.
