@@ -46,8 +46,8 @@ def parse_args():
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--impl", default="svdq", choices=["svdq", "reference"])
     ap.add_argument("--workload", default="mlp_up")
-    ap.add_argument("--format", default="nvfp4", choices=["nvfp4", "int4", "mxfp4", "w8a8"],
-                    help="w8a8 is the 8-bit setting (per-token activations, per-channel weights); "
+    ap.add_argument("--format", default="nvfp4", choices=["nvfp4", "int4", "mxfp4", "w8a8", "fp8"],
+                    help="fp8 is E4M3 with a scale per 128 elements; w8a8 is the 8-bit setting (per-token activations, per-channel weights); "
                          "its rank defaults to 16")
     ap.add_argument("--rank", type=int, default=None)
     ap.add_argument("--no-cpu-baseline", action="store_true")
@@ -347,15 +347,15 @@ def layer_algorithmic(fmt, M, K, N, r):
 
     Prologue: X (2MK), codes and scales, Z (2Mr), L1 (2rK) and lambda (4K).  GEMM: both
     operands' codes and scales, Z, L2 (2Nr), bias (2N) and Y (2MN).  Codes are half a byte
-    per element (W8A8: one); scales one byte per 16 (NVFP4) or 32 (MXFP4) elements, two per
+    per element (W8A8, FP8: one); scales one byte per 16 (NVFP4) or 32 (MXFP4) elements, two per
     64 (INT4 fp16), four per row (W8A8 fp32).
     """
     if fmt == "w8a8":
         code, sc = 1.0, lambda rows: 4.0 * rows
     else:
-        g = {"nvfp4": 16, "mxfp4": 32, "int4": 64}[fmt]
+        g = {"nvfp4": 16, "mxfp4": 32, "int4": 64, "fp8": 128}[fmt]
         per = 2.0 if fmt == "int4" else 1.0
-        code, sc = 0.5, (lambda rows: rows * K / g * per)
+        code, sc = (1.0 if fmt == "fp8" else 0.5), (lambda rows: rows * K / g * per)
     pro = 2.0 * M * K + code * M * K + sc(M) + 2.0 * M * r + 2.0 * r * K + 4.0 * K
     gemm = code * (M + N) * K + sc(M) + sc(N) + 2.0 * M * r + 2.0 * N * r + 2.0 * N + 2.0 * M * N
     return pro, gemm, 2.0 * M * N * K + 2.0 * M * N * r
@@ -725,10 +725,10 @@ def main():
         peak_note = f"dense FP4 = 4 x {peak_src} bf16 burst"
         src = os.path.join(ROOT, "bit_w4a4_quantized_group_b200", "csrc", "gemm_nvfp4.cu")
     else:
-        peak = bf16_burst * 2.0              # dense INT8 = 2 x dense bf16 (nominal ratio 4.5 : 2.25)
-        peak_note = f"dense INT8 = 2 x {peak_src} bf16 burst"
+        peak = bf16_burst * 2.0              # dense INT8, FP8 = 2 x dense bf16 (nominal ratio 4.5 : 2.25)
+        peak_note = f"dense {'FP8' if fmt == 'fp8' else 'INT8'} = 2 x {peak_src} bf16 burst"
         src = os.path.join(ROOT, "bit_w4a4_quantized_group_b200", "csrc",
-                           "gemm_w8a8.cu" if fmt == "w8a8" else "gemm_int4.cu")
+                           {"w8a8": "gemm_w8a8.cu", "int4": "gemm_int4.cu", "fp8": "gemm_fp8.cu"}[fmt])
     alg_flops = flops + 2.0 * M * N * r
     achieved = alg_flops / t_gemm / 1e12
     traffic = recorded_traffic(src, f"{cfg.name}_{fmt}_r{r}")
@@ -737,9 +737,10 @@ def main():
         # L2), one byte per code, one fp32 scale per row
         pro_bytes = 2 * M * K + M * K + 4 * M + 2 * M * r + 2 * r * K + (4 * K)
     else:
-        g = {"nvfp4": 16, "mxfp4": 32, "int4": 64}[fmt]
+        g = {"nvfp4": 16, "mxfp4": 32, "int4": 64, "fp8": 128}[fmt]
         sf = 2 if fmt == "int4" else 1
-        pro_bytes = 2 * M * K + M * K / 2 + M * K / g * sf + 2 * M * r + 2 * r * K + (4 * K)
+        code = 1 if fmt == "fp8" else 0.5
+        pro_bytes = 2 * M * K + code * M * K + M * K / g * sf + 2 * M * r + 2 * r * K + (4 * K)
     out = {
         "metric": METRIC, "value": value, "unit": UNIT, "n_gpus": world, "steps": args.steps,
         "warmup": args.warmup, "ms_per_step": t_step * 1e3, "higher_is_better": True, "scaling": "weak",
@@ -755,7 +756,7 @@ def main():
         "prologue": {"bound": "hbm", "GB/s": pro_bytes / t_pro / 1e9, "peak": hbm,
                      "frac": pro_bytes / t_pro / 1e9 / hbm, "bytes": pro_bytes,
                      "traffic": recorded_traffic(os.path.join(ROOT, "bit_w4a4_quantized_group_b200", "csrc",
-                                                              "prologue.cu"),
+                                                              "prologue_fp8.cu" if fmt == "fp8" else "prologue.cu"),
                                                  f"prologue_{cfg.name}_{fmt}_r{r}")},
         "fusion": None if not fusion else {
             "layer_r0_us": t_r0 * 1e6, "fused_layer_us": t_step * 1e6,
