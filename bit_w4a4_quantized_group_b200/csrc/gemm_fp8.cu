@@ -45,18 +45,22 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);      // 384: up to 168 re
 constexpr uint32_t kABytes = kRows * 128;
 constexpr uint32_t kSfBlk = 512;              // scales of 128 rows x 4 groups
 constexpr int kSfBufs = 4;
-constexpr uint32_t kSfBufCols = 12;           // A-scales 4 columns, B-scales up to 8
 constexpr uint32_t kTmemCols = 512;
 
 template <int BN>
 struct Cfg {
-  static constexpr int kBRows = BN / 2;                               // B rows per CTA
-  static constexpr uint32_t kBBytes = kBRows * 128;
-  static constexpr int kSfbBlks = BN > 128 ? 2 : 1;                   // 128-row scale blocks a tile's columns touch
+  static constexpr int kHalves = BN > 256 ? 2 : 1;                    // MMAs across the tile
+  static constexpr int kN = BN / kHalves;                             // columns of an MMA
+  static constexpr int kSteps = BN > 256 ? 1 : 2;                     // K steps per ring slot
+  static constexpr int kBRows = kN / 2;                               // B rows per CTA and MMA
+  static constexpr uint32_t kBHalfBytes = kBRows * 128;
+  static constexpr uint32_t kBBytes = kHalves * kBHalfBytes;          // ... per step
+  static constexpr int kSfbBlks = (BN + 127) / 128;                   // 128-row scale blocks a tile's columns touch
   static constexpr uint32_t kSfBytes = (1 + kSfbBlks) * kSfBlk;
-  static constexpr uint32_t kStageBytes = 2 * (kABytes + kBBytes);     // [A step 0][A step 1][B step 0][B step 1]
-  static constexpr int kStages = BN >= 192 ? 3 : BN == 128 ? 4 : 5;
-  static constexpr int kAccs = BN == 256 ? 1 : 2;                     // accumulators in TMEM
+  static constexpr uint32_t kSfBufCols = 4 + 4 * kSfbBlks;            // A-scales 4 columns, B-scales 4 per block
+  static constexpr uint32_t kStageBytes = kSteps * (kABytes + kBBytes);   // [A steps][B half 0 steps][B half 1 steps]
+  static constexpr int kStages = BN == 384 ? 5 : BN >= 192 ? 3 : BN == 128 ? 4 : 5;
+  static constexpr int kAccs = BN >= 256 ? 1 : 2;                     // accumulators in TMEM
   static constexpr uint32_t kTmemSf0 = kAccs * BN;
   static constexpr int kColsPerWarp = BN / 2;                         // epilogue columns of a warp
   static_assert(kTmemSf0 + kSfBufs * kSfBufCols <= kTmemCols, "TMEM");
@@ -106,8 +110,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cluster = blockIdx.x >> 1;
   const int nclusters = gridDim.x >> 1;
   const int nk = p.K / kKTile;
-  const int nd = (nk + 1) / 2;                       // double steps: slots of the 8-bit product per tile
+  const int nd = (nk + C::kSteps - 1) / C::kSteps;   // slots of the 8-bit product per tile
   const int nk_lr = (p.rank + 63) / 64;              // ... and one per 64 columns of the branch
+  constexpr int kSfSlots = 4 / C::kSteps;            // slots that a scale block serves
   const TileSeq tiles(p.num_tiles, p.tiles_n, cluster, nclusters);
 
   if (threadIdx.x == 0) {
@@ -156,30 +161,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < tiles.count && ok; ++j) {
         const int m0 = tiles.mb(j) * kBM + static_cast<int>(rank) * kRows;     // this CTA's A rows
         const int n0 = tiles.nb(j) * BN;
-        const int nb0 = n0 + static_cast<int>(rank) * C::kBRows;               // this CTA's B rows
+        const int nb0 = n0 + static_cast<int>(rank) * C::kBRows;               // this CTA's B rows (+ kN for half 1)
         for (int d = 0; d < nd + nk_lr; ++d) {
           if (!wait_bounded(&sh->empty[s], ph, abort_flag, p.err, kErrSiteGemmEmpty)) { ok = false; break; }
-          if (d < nd && (d & 1) == 0) {
+          if (d < nd && d % kSfSlots == 0) {
             // the scale blocks of the next four steps
             if (!wait_bounded(&sh->sf_free[b], sfph, abort_flag, p.err, kErrSiteGemmSfFree)) { ok = false; break; }
             const uint32_t sf_leader = ptx::mapa_shared(ptx::smem_u32(&sh->sf_full[b]), 0);
             const uint32_t sf = ptx::smem_u32(sf_smem + b * C::kSfBytes);
             if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->sf_full[b], 2 * C::kSfBytes);
-            ptx::tma_load_3d_pair_hint(sf, &tmap_sfa, sf_leader, 0, d >> 1, m0 >> 7, keep);
-            ptx::tma_load_3d_pair_hint(sf + kSfBlk, &tmap_sfb, sf_leader, 0, d >> 1, n0 >> 7, keep);
+            ptx::tma_load_3d_pair_hint(sf, &tmap_sfa, sf_leader, 0, d / kSfSlots, m0 >> 7, keep);
+            ptx::tma_load_3d_pair_hint(sf + kSfBlk, &tmap_sfb, sf_leader, 0, d / kSfSlots, n0 >> 7, keep);
             if (++b == kSfBufs) { b = 0; sfph ^= 1u; }
           }
           const uint32_t full_leader = ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0);
           const uint32_t st = ptx::smem_u32(smem + s * C::kStageBytes);
           if (d < nd) {
-            // one load per operand: steps 2d and 2d + 1 (a missing second step reads as zeros)
+            // one load per operand and half: all steps of the slot (a missing second step reads as zeros)
             if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->full[s], 2 * C::kStageBytes);
-            ptx::tma_load_3d_pair_hint(st, &tmap_a, full_leader, 0, m0, 2 * d, keep);
-            ptx::tma_load_3d_pair_hint(st + 2 * kABytes, &tmap_b, full_leader, 0, nb0, 2 * d, keep);
+            ptx::tma_load_3d_pair_hint(st, &tmap_a, full_leader, 0, m0, C::kSteps * d, keep);
+#pragma unroll
+            for (int hh = 0; hh < C::kHalves; ++hh)
+              ptx::tma_load_3d_pair_hint(st + C::kSteps * (kABytes + hh * C::kBHalfBytes), &tmap_b, full_leader, 0,
+                                         nb0 + hh * C::kN, C::kSteps * d, keep);
           } else {
-            if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->full[s], C::kStageBytes);
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&sh->full[s], 2 * (kABytes + C::kBBytes));
             ptx::tma_load_2d_pair(st, &tmap_z, full_leader, (d - nd) * 64, m0);
-            ptx::tma_load_2d_pair(st + 2 * kABytes, &tmap_l2, full_leader, (d - nd) * 64, nb0);
+#pragma unroll
+            for (int hh = 0; hh < C::kHalves; ++hh)
+              ptx::tma_load_2d_pair(st + C::kSteps * (kABytes + hh * C::kBHalfBytes), &tmap_l2, full_leader,
+                                    (d - nd) * 64, nb0 + hh * C::kN);
           }
           if (++s == C::kStages) { s = 0; ph ^= 1u; }
         }
@@ -193,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, b = 0;
       uint32_t ph = 0, sfph = 0;           // parities of the ring slot and of the scale buffer
       bool ok = true;
-      const uint32_t id16 = idesc_bf16(kBM, BN);
+      const uint32_t id16 = idesc_bf16(kBM, C::kN);
       const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem));   // + bytes / 16 for any slot
       for (int j = 0; j < tiles.count && ok; ++j) {
         const int a = C::kAccs == 2 ? (j & 1) : 0;
@@ -206,34 +217,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int d = 0; d < nd + nk_lr; ++d) {
           if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) { ok = false; break; }
           const bool main_slot = d < nd;
-          if (main_slot && (d & 1) == 0 &&
+          if (main_slot && d % kSfSlots == 0 &&
               !wait_bounded(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const bool sf_done = main_slot && ((d & 1) == 1 || d == nd - 1);
+          const bool sf_done = main_slot && (d % kSfSlots == kSfSlots - 1 || d == nd - 1);
           if (ptx::elect_one()) {
             const uint64_t ad = desc0 + static_cast<uint64_t>(s) * (C::kStageBytes / 16);
-            const uint64_t bd = ad + 2 * kABytes / 16;
+            const uint64_t bd = ad + C::kSteps * kABytes / 16;
             if (main_slot) {
-              const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
+              const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * C::kSfBufCols;
               const uint32_t sfb = sfa + 4 + sfb_skip;
-              const uint32_t id0 = static_cast<uint32_t>(d & 1) * 2;    // byte of the scale columns
+              const uint32_t id0 = static_cast<uint32_t>(d % kSfSlots) * C::kSteps;    // byte of the scale columns
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
+              for (int h = 0; h < C::kSteps; ++h) {
                 if (h == 1 && 2 * d + 1 == nk) break;                   // an odd last step
                 const uint32_t id = id0 + h;
-                const uint32_t idesc = idesc_mxf8(kBM, BN, 0) | (id << 29) | (id << 4);
+                const uint32_t idesc = idesc_mxf8(kBM, C::kN, 0) | (id << 29) | (id << 4);
 #pragma unroll
-                for (int q = 0; q < kKTile / 32; ++q)
-                  ptx::umma_mxf8_pair(acc, ad + h * (kABytes / 16) + 2 * q, bd + h * (C::kBBytes / 16) + 2 * q, idesc,
-                                      sfa | (id << 30), sfb | (id << 30), (d | h | q) != 0 ? 1u : 0u);
+                for (int hh = 0; hh < C::kHalves; ++hh)
+#pragma unroll
+                  for (int q = 0; q < kKTile / 32; ++q)
+                    ptx::umma_mxf8_pair(acc + hh * C::kN, ad + h * (kABytes / 16) + 2 * q,
+                                        bd + (hh * C::kSteps + h) * (C::kBHalfBytes / 16) + 2 * q, idesc, sfa | (id << 30),
+                                        (sfb + hh * (C::kN / 32)) | (id << 30), (d | h | q) != 0 ? 1u : 0u);
               }
               if (sf_done) ptx::tc_commit_pair(&sh->sf_free[b], 0x3);
             } else {
               const int nmma = min(64, p.rank - (d - nd) * 64) / 16;
-              for (int q = 0; q < nmma; ++q) ptx::umma_f16_pair(acc, ad + 2 * q, bd + 2 * q, id16, 1u);
+#pragma unroll
+              for (int hh = 0; hh < C::kHalves; ++hh)
+                for (int q = 0; q < nmma; ++q)
+                  ptx::umma_f16_pair(acc + hh * C::kN, ad + 2 * q, bd + hh * C::kSteps * (C::kBHalfBytes / 16) + 2 * q,
+                                     id16, 1u);
             }
             ptx::tc_commit_pair(&sh->empty[s], 0x3);
             if (d == nd + nk_lr - 1) ptx::tc_commit_pair(&sh->acc_full[a], 0x3);
@@ -258,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t sd = sfdesc0 + static_cast<uint64_t>(b) * (C::kSfBytes / 16);
-          const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * kSfBufCols;
+          const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * C::kSfBufCols;
           ptx::tmem_cp_32x128b_warpx4_pair(sfa, sd);
 #pragma unroll
           for (int q = 0; q < C::kSfbBlks; ++q)
@@ -279,27 +297,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t use = static_cast<uint32_t>(C::kAccs == 2 ? j >> 1 : j);
       const int m0 = tiles.mb(j) * kBM + static_cast<int>(rank) * kRows;
       const int col0 = tiles.nb(j) * BN + h * C::kColsPerWarp;
+      if (NC > 4 && p.bias && lane < 3 && col0 + lane * 64 < p.N) {
+        // the bias is read before the release here: have its lines in L1 by then
+        const unsigned short touch = __ldg(reinterpret_cast<const unsigned short*>(p.bias) + col0 + lane * 64);
+        asm volatile("" ::"h"(touch));
+      }
       if (!wait_bounded(&sh->acc_full[a], use & 1u, abort_flag, p.err, kErrSiteGemmAccFull)) break;
       ptx::tc_fence_after();
-      // the warp's columns into registers, then the accumulator goes back to the MMA warp at once
-      uint32_t v[NC][32];
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * BN + h * C::kColsPerWarp;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) ptx::tmem_ld_32x32b_x32(base + c * 32, v[c]);
-      ptx::tmem_wait_ld();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_peer(ptx::mapa_shared(ptx::smem_u32(&sh->acc_empty[a]), 0));
       const int row = m0 + q * 32 + lane;
-      if (row >= p.M) continue;
       __nv_bfloat16* yrow = p.Y + static_cast<size_t>(row) * p.N + col0;
-#pragma unroll
-      for (int c16 = 0; c16 < 2 * NC; ++c16) {
-        const int cl = c16 * 16;
-        if (col0 + cl >= p.N) break;                       // the last tile may reach past N
-        const bool in_n = SVDQ_IN_GLOBAL(col0 + cl + 16 <= p.N, p.err);
+      auto release = [&]() {       // the accumulator goes back to the MMA warp
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_peer(ptx::mapa_shared(ptx::smem_u32(&sh->acc_empty[a]), 0));
+      };
+      // 16 columns: + bias -> bf16 pairs
+      auto convert = [&](const uint32_t* v, int cl, uint32_t* o) {
         float bv[16];
-        if (p.bias && in_n) {
+        if (p.bias && SVDQ_IN_GLOBAL(col0 + cl >= p.N || col0 + cl + 16 <= p.N, p.err) && col0 + cl < p.N) {
 #pragma unroll
           for (int hb = 0; hb < 2; ++hb) {
             const uint4 braw = __ldg(reinterpret_cast<const uint4*>(p.bias + col0 + cl + 8 * hb));
@@ -314,20 +330,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) bv[e] = 0.f;
         }
-        uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const __nv_bfloat162 hv = __floats2bfloat162_rn(__uint_as_float(v[cl / 32][cl % 32 + 2 * e]) + bv[2 * e],
-                                                          __uint_as_float(v[cl / 32][cl % 32 + 2 * e + 1]) + bv[2 * e + 1]);
+          const __nv_bfloat162 hv = __floats2bfloat162_rn(__uint_as_float(v[2 * e]) + bv[2 * e],
+                                                          __uint_as_float(v[2 * e + 1]) + bv[2 * e + 1]);
           o[e] = *reinterpret_cast<const uint32_t*>(&hv);
         }
-        if (!in_n) {
-        } else if (p.y_align32) {
+      };
+      auto store = [&](const uint32_t (&o)[8], int cl) {
+        if (row >= p.M || col0 + cl >= p.N) return;          // the last tiles may reach past M and N
+        if (!SVDQ_IN_GLOBAL(col0 + cl + 16 <= p.N, p.err)) return;
+        if (p.y_align32) {
           ptx::st_global_v8_na(yrow + cl, o);
         } else {
           *reinterpret_cast<uint4*>(yrow + cl) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4*>(yrow + cl + 8) = make_uint4(o[4], o[5], o[6], o[7]);
         }
+      };
+      if constexpr (NC <= 4) {
+        // the warp's columns into registers as they are, converted after the release
+        uint32_t v[NC][32];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) ptx::tmem_ld_32x32b_x32(base + c * 32, v[c]);
+        ptx::tmem_wait_ld();
+        release();
+#pragma unroll
+        for (int c16 = 0; c16 < 2 * NC; ++c16) {
+          uint32_t o[8];
+          convert(&v[c16 / 2][c16 % 2 * 16], c16 * 16, o);
+          store(o, c16 * 16);
+        }
+      } else {
+        // 192 columns: as bf16 pairs, since the registers do not hold that many fp32 values
+        uint32_t o[2 * NC][8];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(base + c * 32, v);
+          ptx::tmem_wait_ld();
+          convert(v, c * 32, o[2 * c]);
+          convert(v + 16, c * 32 + 16, o[2 * c + 1]);
+        }
+        release();
+#pragma unroll
+        for (int c16 = 0; c16 < 2 * NC; ++c16) store(o[c16], c16 * 16);
       }
     }
   }
@@ -414,7 +460,7 @@ float gemm_fp8_tile(int M, int N, int K, int num_sms, int* bn) {
   const int64_t slots = num_sms / 2 > 0 ? num_sms / 2 : 1;
   float best = 0.f;
   *bn = 0;
-  for (int w : {256, 192, 128, 64}) {
+  for (int w : {384, 256, 192, 128, 64}) {
     const int64_t tiles = tm * ((N + w - 1) / w);
     const float t = 4.f + static_cast<float>((tiles + slots - 1) / slots * (K / kKTile)) * (0.13f + 0.00153f * w);
     if (*bn == 0 || t < best) {
@@ -429,6 +475,7 @@ cudaError_t launch_gemm_fp8(int bn, const CUtensorMap& ta, const CUtensorMap& tb
                             const CUtensorMap& tsfb, const CUtensorMap& tz, const CUtensorMap& tl2,
                             const GemmParams& p, int num_sms, cudaStream_t s) {
   switch (bn) {
+    case 384: return launch<384>(ta, tb, tsfa, tsfb, tz, tl2, p, num_sms, s);
     case 256: return launch<256>(ta, tb, tsfa, tsfb, tz, tl2, p, num_sms, s);
     case 192: return launch<192>(ta, tb, tsfa, tsfb, tz, tl2, p, num_sms, s);
     case 128: return launch<128>(ta, tb, tsfa, tsfb, tz, tl2, p, num_sms, s);

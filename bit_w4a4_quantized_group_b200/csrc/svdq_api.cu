@@ -356,14 +356,14 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
     const int small = gemm_fp8_small_tokens(p.M, p.N, p.K, sms, pair_us);
     if (small) bn = 128;
     const uint32_t xrows = small ? static_cast<uint32_t>(small) : 128u;
-    const uint32_t wrows = small ? 128u : static_cast<uint32_t>(bn / 2);
-    const uint32_t wblocks = !small && bn > 128 ? 2 : 1;
+    const uint32_t wrows = small ? 128u : static_cast<uint32_t>(bn > 256 ? bn / 4 : bn / 2);
+    const uint32_t wblocks = small ? 1 : static_cast<uint32_t>((bn + 127) / 128);
     p.tiles_m = static_cast<int>(small ? (M + small - 1) / small : (M + 255) / 256);
     p.tiles_n = static_cast<int>((N + bn - 1) / bn);
     p.num_tiles = p.tiles_m * p.tiles_n;
     CUtensorMap ta, tb, tsfa, tsfb;
-    // rows seen as [K/128 steps][rows][128 bytes]; the large tiles load two steps per box
-    const uint32_t steps = small ? 1 : 2;
+    // rows seen as [K/128 steps][rows][128 bytes]; the tiles up to 256 wide load two steps per box
+    const uint32_t steps = small || bn > 256 ? 1 : 2;
     if (!make_tmap_3d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 128, M, K / 128, K, 128, 128, xrows, steps,
                       CU_TENSOR_MAP_SWIZZLE_128B))
       return SVDQ_ERR_CUDA;

@@ -206,7 +206,7 @@ size_t gemm_int4_smem_bytes();
 cudaError_t launch_gemm_w8a8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tz,
                              const CUtensorMap& tl2, const CUtensorMap& ty, const GemmParams& p, int num_sms,
                              cudaStream_t s);
-// FP8 GEMM: CTA-pair tiles of 256 x bn.  gemm_fp8_tile picks bn (64, 128, 192 or 256) and returns the
+// FP8 GEMM: CTA-pair tiles of 256 x bn.  gemm_fp8_tile picks bn (64, 128, 192, 256 or 384) and returns the
 // estimated time in us.
 float gemm_fp8_tile(int M, int N, int K, int num_sms, int* bn);
 cudaError_t launch_gemm_fp8(int bn, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsfa,

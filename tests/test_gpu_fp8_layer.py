@@ -111,7 +111,9 @@ def test_gemm_branch_and_bias(M, N, K, rank):
 
 @pytest.mark.parametrize("M,N,K,rank", [(2048, 2304, 384, 16), (1024, 3328, 640, 48), (512, 4608, 1152, 0),
                                         (1000, 3456, 128, 32), (4608, 1152, 256, 0), (3000, 6144, 1664, 16),
-                                        (1, 9216, 4096, 16), (40, 12288, 512, 0), (5000, 128, 128, 0)])
+                                        (1, 9216, 4096, 16), (40, 12288, 512, 0), (5000, 128, 128, 0),
+                                        (2048, 2944, 640, 48), (2000, 2816, 1152, 16), (1800, 3072, 128, 0),
+                                        (2048, 4096, 256, 128), (4608, 5888, 2176, 0)])
 def test_gemm_many_tiles(M, N, K, rank):
     _gemm(M, N, K, rank, rank > 0, seed=N)
 
