@@ -10,13 +10,17 @@
 // elements of K.
 //
 // Design:
-//   * clusters of two CTAs compute 256 x BN output tiles with cta_group::2 MMAs, each CTA
-//     holding 128 rows of A and BN/2 rows of B; persistent clusters take contiguous runs of the
-//     N-fastest tile numbering;
-//   * a ring slot holds two K steps of 128 bytes per row of A and B, each operand brought by one 3-D
-//     TMA load ([K/128 chunks][rows][128 bytes], two chunks per box) and counted on a barrier of the
-//     leader CTA (each CTA loads into its own shared memory; no multicast loads).  The MMA warp's
-//     own work per slot (waits, issue, commit) is of the order of 400 cycles, so that slots of one
+//   * clusters of two CTAs compute 256 x BN output tiles, BN = 64, 128, 192, 256 or 384 (the last as
+//     two MMAs of 192 columns that share A), with cta_group::2 MMAs, each CTA holding 128 rows of A
+//     and BN/2 rows of B; persistent clusters take contiguous runs of the N-fastest tile numbering.
+//     What bounds large products is power: at 1000 W the SM clock falls to 1.3 GHz, and the energy
+//     of moving operands from L2 counts beside that of the MMAs.  A step moves 128 + BN/2 rows per
+//     SM for 128 x BN outputs, so 384 columns save 17% of the bytes of 256: 155 -> 144 us at
+//     4608 x 12288 x 3072 back to back, 475 -> 427 at 16384 x 3072 x 9216;
+//   * a ring slot holds two K steps (384 columns: one) of 128 bytes per row of A and B, each operand
+//     brought by one 3-D TMA load ([K/128 chunks][rows][128 bytes], two chunks per box) and counted
+//     on a barrier of the leader CTA (each CTA loads into its own shared memory; no multicast
+//     loads).  The MMA warp's own work per slot (waits, issue, commit) is of the order of 400 cycles, so that slots of one
 //     step kept the tensor pipe waiting: 512 cycles of MMAs at BN = 256, 128 at BN = 64;
 //   * the scale blocks (512 bytes per 128 rows and four steps) have a ring of their own: a copy
 //     warp of the leader moves them into the TMEM buffer of the same number (two or three
@@ -24,8 +28,8 @@
 //   * ceil(r/64) further slots hold Z and L2 (bf16): kind::f16 MMAs add the branch onto the same
 //     accumulator;
 //   * eight epilogue warps per CTA drain TMEM into registers, hand the accumulator back, add the
-//     bias and store bf16 Y while the next tile's MMAs run.  BN < 256 leaves TMEM for two
-//     accumulators, so that the next tile's MMAs do not wait for the drain either.
+//     bias and store bf16 Y while the next tile's MMAs run.  192 columns and fewer leave TMEM for
+//     two accumulators, so that the next tile's MMAs do not wait for the drain either.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -140,7 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
-  // the set-up above may overlap the end of the kernel that writes A and Z
+  // the next kernel may set itself up on SMs that this grid leaves free; the set-up above may itself
+  // have overlapped the end of the kernel that writes A and Z
+  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
 
   if (warp == kProdWarp) {
@@ -454,8 +460,9 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorM
 float gemm_fp8_tile(int M, int N, int K, int num_sms, int* bn) {
   // The tile width with the least time.  Waves of the persistent clusters times K steps times the time
   // of a step, 0.13 us + 1.53 ns per column, and 4 us to start and drain.  Measured back to back, us a
-  // step for widths 256, 192, 128 and 64: 0.52, 0.43, 0.32 and 0.23 at 4608 x 12288 x 3072; whole calls
-  // 7.8 us at 300 x 2176 x 1152 (64 wide), 12.0 at 256 x 3072 x 9216 (128), 12.9 at 1024 x 3072 x 3072 (192).
+  // step for widths 384, 256, 192, 128 and 64: 0.75, 0.54, 0.43, 0.32 and 0.23 at 4608 x 12288 x 3072;
+  // whole calls 7.8 us at 300 x 2176 x 1152 (64 wide), 12.0 at 256 x 3072 x 9216 (128), 12.9 at 1024 x
+  // 3072 x 3072 (192), 22.9 at 2048 x 3072 x 3072 (384; 24.9 with 256).
   const int64_t tm = (M + kBM - 1) / kBM;
   const int64_t slots = num_sms / 2 > 0 ? num_sms / 2 : 1;
   float best = 0.f;

@@ -14,7 +14,7 @@ sys.path.insert(0, ROOT)
 # (M, K, N, rank): one token, ragged token counts of every tile width, odd and even K steps, a K
 # whose steps outnumber the ring, tiles that reach past N
 SHAPES = [(1, 128, 128, 0), (1, 2048, 256, 16), (17, 640, 384, 0), (40, 4096, 128, 48), (100, 8192, 256, 0),
-          (129, 384, 384, 16), (300, 640, 640, 48), (700, 1152, 3456, 0), (1025, 256, 3328, 16)]
+          (129, 384, 384, 16), (300, 640, 640, 48), (700, 1152, 3456, 0), (1025, 256, 3328, 16), (2048, 384, 2944, 16)]
 
 
 def main(lib_path: str, out: str) -> None:
