@@ -42,6 +42,12 @@ __device__ __forceinline__ uint4 ld_global_v4_na(const void* p) {
   return v;
 }
 
+// Larger of two unsigned 16-bit halves each, one instruction.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Maximum over the 16 lanes that hold one group (8 elements each).
 __device__ __forceinline__ float group_max16(float a) {
   a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));

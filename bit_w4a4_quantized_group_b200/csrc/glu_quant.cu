@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
   for (int i = 0; i < kRows / 2; ++i) {
     sb[i] = fp8_scale_byte(amax[2 * i]) | (fp8_scale_byte(amax[2 * i + 1]) << 16);
 #pragma unroll
-    for (int o = 1; o <= 4; o <<= 1) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
+    for (int o = 1; o <= 4; o <<= 1) sb[i] = max_u16x2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
   }
   if (!on) return;
 #pragma unroll

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_fp8_kernel(const __nv_bflo
 #pragma unroll
   for (int o = 1; o <= 8; o <<= 1) {
 #pragma unroll
-    for (int i = 0; i < kQRows / 2; ++i) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
+    for (int i = 0; i < kQRows / 2; ++i) sb[i] = max_u16x2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
   }
   if (!on) return;
 #pragma unroll
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
       for (int o = 1; o <= 8; o <<= 1) {
 #pragma unroll
-        for (int i = 0; i < kR / 2; ++i) sb[i] = __vmaxu2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
+        for (int i = 0; i < kR / 2; ++i) sb[i] = max_u16x2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
       }
       uint8_t* dst = p.codes + static_cast<size_t>(m0 + r0) * p.K + grp * 128 + c * 8;
 #pragma unroll
