@@ -89,8 +89,11 @@ def _bind_calls(lib):
     from importlib.machinery import ExtensionFileLoader
     from importlib.util import module_from_spec, spec_from_loader
     loader = ExtensionFileLoader("svdq_call", CALLS_PATH)
-    mod = module_from_spec(spec_from_loader("svdq_call", loader))
-    loader.exec_module(mod)
+    try:
+        mod = module_from_spec(spec_from_loader("svdq_call", loader))
+        loader.exec_module(mod)
+    except ImportError:              # built for another Python
+        return lib
     mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
                ("svdq_quantize_act_lowrank_down", "svdq_w4a4_gemm_lowrank_up", "svdq_rmsnorm_quantize_act",
                 "svdq_glu_quantize_act")))

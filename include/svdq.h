@@ -248,7 +248,7 @@ svdq_status svdq_rmsnorm_quantize_act(svdq_format fmt, int64_t M, int64_t K,
  * gate and up are [M][K] with rows ldg and ldu elements apart (each >= K and a multiple of
  * 8), so that both may be column slices of one wider GEMM output; up NULL means no gating
  * (ldu is then ignored).  lambda is fp32 [K] as in svdq_quantize_act_lowrank_down, or NULL.
- * act is evaluated to a few units in the last place of fp32.
+ * y is evaluated in fp32 with a relative error below 2^-15; values below 2^-110 may become 0.
  * The outputs feed svdq_w4a4_gemm_lowrank_up with rank 0.
  */
 svdq_status svdq_glu_quantize_act(svdq_format fmt, svdq_activation act, int64_t M, int64_t K,

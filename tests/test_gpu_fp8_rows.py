@@ -6,9 +6,10 @@ most delta relatively.  delta is the fp32 error of the formula, in units of 2^-2
   norm  the sum of squares adds at most 8 * 4 products per thread (or K/1024 in the looping form,
         K <= 40960 here: 40), 5 + 5 tree steps: at most 50; halved by the square root, plus the
         divide, the addition of eps, the root and two products: 50 / 2 + 5 <= 32 = 2^5: 2^-19;
-  glu   exp has 2 + 1.173 |t| units in the last place (2 units of 2^-24 each), |t| <= 88 wherever
-        the result is not below 2^-120, and the rounded argument of the GELU form adds 3 |t|:
-        2 * 106 + 3 * 88 + 10 < 512 = 2^9: 2^-15; below that, 2^-110 absolutely.
+  glu   exp(-t) is 2^a of an argument with at most four roundings, |a| <= 127 wherever the result is
+        not below 2^-110: ln 2 * 127 * 4 = 352 units, 4 more for the hardware's 2^a (2^-22), 2 for
+        its reciprocal and 4 for the sum and the products: < 512 = 2^9: 2^-15; below that, 2^-110
+        absolutely.
 """
 import numpy as np
 import pytest
