@@ -13,7 +13,8 @@
 // thread has two 16-byte chunks of it (64 elements apart, so that the lanes of a load are
 // neighbours) in each of kRows rows, all its loads in flight together.  The exponentials and
 // reciprocals (two per element, 16 a clock and SM) and the instruction issue are each busy about as
-// long as memory, so products run on pairs (f32x2) and row overheads are spread over 16 elements.
+// long as memory, so products run on pairs (f32x2), row overheads are spread over 16 elements, and
+// large ungated calls fetch a thread's next rows under the stores of the current ones.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -29,6 +30,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kGroups = kThreads / 8;          // 128-element groups across a CTA
 constexpr int kRows = 2;
+constexpr int kIters = 4;
 
 // -t log2(e) of a pair: the factor -log2(e) is folded into the constants, so that exp(-t) is one ex2.
 template <int ACT>
@@ -48,118 +50,134 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-template <int ACT, bool GATED, bool LAM>
+// ITERS row pairs per CTA, one after the other, the next pair's loads under the current one's stores.
+template <int ACT, bool GATED, bool LAM, int ITERS>
 __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int t = static_cast<int>(threadIdx.x);
   const int G = p.K >> 7;
   const int cblocks = (G + kGroups - 1) / kGroups;
-  const int row0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(cblocks)) * kRows;
+  const int row0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(cblocks)) * (kRows * ITERS);
   const int grp = static_cast<int>(blockIdx.x % static_cast<unsigned>(cblocks)) * kGroups + (t >> 3);
   if (row0 >= p.M) {      // the CTA behind the last row block
     fp8_zero_padding(p.scales, p.M, p.K, p.sfb, t, kThreads);
     return;
   }
   const bool on = grp < G;
-  const int rows = min(kRows, p.M - row0);
+  const int row_end = min(p.M, row0 + kRows * ITERS);
   const size_t col = static_cast<size_t>(grp) * 128 + (t & 7) * 8;     // and col + 64
   uint4 g[kRows][2], u[GATED ? kRows : 1][2];
+  auto load = [&](int r) {
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const bool in = on && i < rows;
-    const __nv_bfloat16* src = p.gate + static_cast<size_t>(row0 + i) * p.ldg + col;
+    for (int i = 0; i < kRows; ++i) {
+      const bool in = on && r + i < row_end;
+      const __nv_bfloat16* src = p.gate + static_cast<size_t>(r + i) * p.ldg + col;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) g[i][h] = in ? ld_global_v4_na(src + 64 * h) : make_uint4(0, 0, 0, 0);
-    if (GATED) {
-      const __nv_bfloat16* srcu = p.up + static_cast<size_t>(row0 + i) * p.ldu + col;
+      for (int h = 0; h < 2; ++h) g[i][h] = in ? ld_global_v4_na(src + 64 * h) : make_uint4(0, 0, 0, 0);
+      if (GATED) {
+        const __nv_bfloat16* srcu = p.up + static_cast<size_t>(r + i) * p.ldu + col;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) u[i][h] = in ? ld_global_v4_na(srcu + 64 * h) : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < 2; ++h) u[i][h] = in ? ld_global_v4_na(srcu + 64 * h) : make_uint4(0, 0, 0, 0);
+      }
     }
-  }
-  // y of every row, and the scale byte that this thread's own elements need.  The byte grows with the
-  // absolute value, so the group's byte is the largest of its lanes': two rows' bytes go through one
-  // shuffle as 16-bit halves.
-  float2 y[kRows][8];
-  float amax[kRows];
+  };
+  load(row0);
+#pragma unroll 1
+  for (int r = row0; r < row_end; r += kRows) {
+    const int rows = min(kRows, row_end - r);
+    // y of every row, and the scale byte that this thread's own elements need.  The byte grows with the
+    // absolute value, so the group's byte is the largest of its lanes': two rows' bytes go through one
+    // shuffle as 16-bit halves.
+    float2 y[kRows][8];
+    float amax[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) amax[i] = 0.f;
+    for (int i = 0; i < kRows; ++i) amax[i] = 0.f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float2 lam[4];
-    if (LAM) {
-      const float4* lp = reinterpret_cast<const float4*>(p.lam + (on ? col : 0) + 64 * h);
-      const float4 l0 = __ldg(lp), l1 = __ldg(lp + 1);
-      lam[0] = make_float2(l0.x, l0.y);
-      lam[1] = make_float2(l0.z, l0.w);
-      lam[2] = make_float2(l1.x, l1.y);
-      lam[3] = make_float2(l1.z, l1.w);
+    for (int h = 0; h < 2; ++h) {
+      float2 lam[4];
+      if (LAM) {
+        const float4* lp = reinterpret_cast<const float4*>(p.lam + (on ? col : 0) + 64 * h);
+        const float4 l0 = __ldg(lp), l1 = __ldg(lp + 1);
+        lam[0] = make_float2(l0.x, l0.y);
+        lam[1] = make_float2(l0.z, l0.w);
+        lam[2] = make_float2(l1.x, l1.y);
+        lam[3] = make_float2(l1.z, l1.w);
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const uint32_t gx[4] = {g[i][h].x, g[i][h].y, g[i][h].z, g[i][h].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = make_float2(bf16x2_lo(gx[e]), bf16x2_hi(gx[e]));
+          const float2 nt = neg_t_log2<ACT>(x);
+          float2 d = __fadd2_rn(make_float2(ex2_approx(nt.x), ex2_approx(nt.y)), make_float2(1.f, 1.f));
+          if (LAM) d = __fmul2_rn(d, lam[e]);           // one reciprocal serves both divides
+          float2 v = __fmul2_rn(x, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+          if (GATED) {
+            const uint32_t ux[4] = {u[i][h].x, u[i][h].y, u[i][h].z, u[i][h].w};
+            v = __fmul2_rn(v, make_float2(bf16x2_lo(ux[e]), bf16x2_hi(ux[e])));
+          }
+          amax[i] = fmaxf(amax[i], fmaxf(fabsf(v.x), fabsf(v.y)));
+          y[i][4 * h + e] = v;
+        }
+      }
+    }
+    if (ITERS > 1) load(r + kRows);
+    uint32_t sb[kRows / 2];
+#pragma unroll
+    for (int i = 0; i < kRows / 2; ++i) {
+      sb[i] = fp8_scale_byte(amax[2 * i]) | (fp8_scale_byte(amax[2 * i + 1]) << 16);
+#pragma unroll
+      for (int o = 1; o <= 4; o <<= 1) sb[i] = max_u16x2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const uint32_t gx[4] = {g[i][h].x, g[i][h].y, g[i][h].z, g[i][h].w};
+      if (i >= rows || !on) break;
+      const int row = r + i;
+      const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+      const float inv = fp8_inv_scale(b);
+      uint8_t* dst = p.codes + static_cast<size_t>(row) * p.K + col;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = make_float2(bf16x2_lo(gx[e]), bf16x2_hi(gx[e]));
-        const float2 nt = neg_t_log2<ACT>(x);
-        float2 d = __fadd2_rn(make_float2(ex2_approx(nt.x), ex2_approx(nt.y)), make_float2(1.f, 1.f));
-        if (LAM) d = __fmul2_rn(d, lam[e]);           // one reciprocal serves both divides
-        float2 v = __fmul2_rn(x, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
-        if (GATED) {
-          const uint32_t ux[4] = {u[i][h].x, u[i][h].y, u[i][h].z, u[i][h].w};
-          v = __fmul2_rn(v, make_float2(bf16x2_lo(ux[e]), bf16x2_hi(ux[e])));
+      for (int h = 0; h < 2; ++h) {
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = __fmul2_rn(y[i][4 * h + e], make_float2(inv, inv));
+          q[e] = ptx::cvt_e4m3x2(v.x, v.y);
         }
-        amax[i] = fmaxf(amax[i], fmaxf(fabsf(v.x), fabsf(v.y)));
-        y[i][4 * h + e] = v;
+        if (SVDQ_IN_GLOBAL(col + 64 * h + 8 <= static_cast<size_t>(p.K), p.err))
+          *reinterpret_cast<uint2*>(dst + 64 * h) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
       }
+      if ((t & 7) == 0) p.scales[fp8_sf_offset(row, grp, p.sfb)] = static_cast<uint8_t>(b);
+      // the row's padding groups, by the lanes of its last group
+      if (grp == G - 1 && (t & 7) > 0 && (t & 7) < 4 * p.sfb - G + 1)
+        p.scales[fp8_sf_offset(row, G - 1 + (t & 7), p.sfb)] = 0;
     }
-  }
-  uint32_t sb[kRows / 2];
-#pragma unroll
-  for (int i = 0; i < kRows / 2; ++i) {
-    sb[i] = fp8_scale_byte(amax[2 * i]) | (fp8_scale_byte(amax[2 * i + 1]) << 16);
-#pragma unroll
-    for (int o = 1; o <= 4; o <<= 1) sb[i] = max_u16x2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
-  }
-  if (!on) return;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (i >= rows) break;
-    const int row = row0 + i;
-    const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
-    const float inv = fp8_inv_scale(b);
-    uint8_t* dst = p.codes + static_cast<size_t>(row) * p.K + col;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t q[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 v = __fmul2_rn(y[i][4 * h + e], make_float2(inv, inv));
-        q[e] = ptx::cvt_e4m3x2(v.x, v.y);
-      }
-      if (SVDQ_IN_GLOBAL(col + 64 * h + 8 <= static_cast<size_t>(p.K), p.err))
-        *reinterpret_cast<uint2*>(dst + 64 * h) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-    }
-    if ((t & 7) == 0) p.scales[fp8_sf_offset(row, grp, p.sfb)] = static_cast<uint8_t>(b);
-    // the row's padding groups, by the lanes of its last group
-    if (grp == G - 1 && (t & 7) > 0 && (t & 7) < 4 * p.sfb - G + 1)
-      p.scales[fp8_sf_offset(row, G - 1 + (t & 7), p.sfb)] = 0;
   }
 }
 
 template <int ACT>
-cudaError_t launch(const GluParams& p, const cudaLaunchConfig_t& cfg) {
-  if (p.up) return p.lam ? cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, true, true>, p)
-                         : cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, true, false>, p);
-  return p.lam ? cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, false, true>, p)
-               : cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, false, false>, p);
+cudaError_t launch(const GluParams& p, int iters, const cudaLaunchConfig_t& cfg) {
+  if (p.up) return p.lam ? cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, true, true, 1>, p)
+                         : cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, true, false, 1>, p);
+  if (iters > 1) return p.lam ? cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, false, true, kIters>, p)
+                              : cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, false, false, kIters>, p);
+  return p.lam ? cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, false, true, 1>, p)
+               : cudaLaunchKernelEx(&cfg, glu_quant_kernel<ACT, false, false, 1>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s) {
   const int64_t cblocks = (p.K / 128 + kGroups - 1) / kGroups;
-  const int64_t grid = cblocks * ((p.M + kRows - 1) / kRows) + (p.M % 128 ? 1 : 0);
+  // Four row pairs per CTA where that still leaves 3000 CTAs, four rounds of the device (GELU 4608 x
+  // 12288: 36.6 us against 38.7; 1000 rows of a small K get slower).  With gating a
+  // pair has twice the loads, and the next pair's registers cost more than they give (2304 x 12288:
+  // 25.9 us against 24.4).
+  const int iters = !p.up && cblocks * ((static_cast<int64_t>(p.M) + 2 * kIters - 1) / (2 * kIters)) >= 3000 ? kIters : 1;
+  const int64_t rows = kRows * iters;
+  const int64_t grid = cblocks * ((p.M + rows - 1) / rows) + (p.M % 128 ? 1 : 0);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -170,7 +188,7 @@ cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = p.act == SVDQ_ACT_SILU ? launch<SVDQ_ACT_SILU>(p, cfg) : launch<SVDQ_ACT_GELU_TANH>(p, cfg);
+  cudaError_t e = p.act == SVDQ_ACT_SILU ? launch<SVDQ_ACT_SILU>(p, iters, cfg) : launch<SVDQ_ACT_GELU_TANH>(p, iters, cfg);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -188,6 +188,20 @@ def test_glu(act, gated, lam, M, K):
     F.check_quantized(codes, sb, _glu64(act, gate, up, lm), GLU_DELTA, GLU_FLOOR)
 
 
+@pytest.mark.parametrize("act,lam,M,K", [("silu", False, 24011, 640), ("gelu", True, 12005, 2304)])
+def test_glu_many_rows(act, lam, M, K):
+    """Enough rows that a thread takes several pairs of them, and a last block that is not full."""
+    gate = _acts(M, K + 8, 5, scale=2.0)[:, 8:]
+    lm = torch.linspace(0.25, 4.0, K, device="cuda") if lam else None
+    codes, sb = _run_glu(act, gate, None, lm)
+    pick = np.r_[0:40, M // 2: M // 2 + 40, M - 40: M]
+    F.check_quantized(codes[pick], sb[pick], _glu64(act, gate[torch.from_numpy(pick).cuda()], None, lm), GLU_DELTA, GLU_FLOOR)
+    # every row: the same bytes as the rows in small calls, which take one pair per thread
+    for i in range(0, M, 3001):
+        part = _run_glu(act, gate[i: i + 3001], None, lm)
+        assert np.array_equal(part[0], codes[i: i + 3001]) and np.array_equal(part[1], sb[i: i + 3001])
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_glu_over_the_whole_range(act):
     """Every finite bf16 value with |x| <= 2^100 as a gate, each alone in its group."""
