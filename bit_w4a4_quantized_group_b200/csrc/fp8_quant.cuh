@@ -48,35 +48,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Maximum over the 16 lanes that hold one group (8 elements each).
-__device__ __forceinline__ float group_max16(float a) {
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
-  return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
-}
-__device__ __forceinline__ float max8(const float (&y)[8]) {
-  return fmaxf(fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))),
-               fmaxf(fmaxf(fabsf(y[4]), fabsf(y[5])), fmaxf(fabsf(y[6]), fabsf(y[7]))));
-}
-
-// Codes and scale of this thread's 8 elements (chunk c of the row) of a group that 16 lanes hold;
-// all lanes of the warp call it, `on` says whether the lane has a chunk (whole groups at a time).
-__device__ __forceinline__ void fp8_store_chunk(const float (&y)[8], bool on, int row, int c, int K, int sfb,
-                                                uint8_t* codes, uint8_t* scales, size_t nscale, int* err) {
-  const float a = group_max16(on ? max8(y) : 0.f);
-  const uint32_t b = fp8_scale_byte(a);
-  const float inv = fp8_inv_scale(b);
-  uint2 q;
-  q.x = ptx::cvt_e4m3x2(y[0] * inv, y[1] * inv) | (ptx::cvt_e4m3x2(y[2] * inv, y[3] * inv) << 16);
-  q.y = ptx::cvt_e4m3x2(y[4] * inv, y[5] * inv) | (ptx::cvt_e4m3x2(y[6] * inv, y[7] * inv) << 16);
-  if (on && SVDQ_IN_GLOBAL(c * 8 + 8 <= K, err)) {
-    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * K + static_cast<size_t>(c) * 8) = q;
-    const size_t so = fp8_sf_offset(row, c >> 4, sfb);
-    if ((c & 15) == 0 && SVDQ_IN_GLOBAL(so < nscale, err)) scales[so] = static_cast<uint8_t>(b);
-  }
-}
-
 // Zero scale bytes of the padding: thread t of n writes its share of the padding rows M .. Mpad-1
 // (a 4-byte word per row and block of groups) and of the padding groups of the rows below M.
 __device__ __forceinline__ void fp8_zero_padding(uint8_t* scales, int M, int K, int sfb, int64_t t, int64_t n) {

@@ -4,10 +4,13 @@
 //   codes = e4m3(y / 2^e), 2^e per 128 elements (fp8_quant.cuh).
 //
 // What bounds it: memory.  x and r are read once, h and the codes are written once: 7 bytes per
-// element with a residual, 3 without, and a few dozen instructions.  One CTA holds one row in
-// registers (8 elements per 16-byte load, as bf16 pairs, so that a row of 32768 elements fits
-// 1024 threads), adds the squares over the CTA, and quantizes from the registers: no second
-// read.  Sixteen neighbouring lanes hold a group of 128, so its maximum takes four shuffles.
+// element with a residual, 3 without.  One CTA holds one row in registers as bf16, adds the squares
+// over the CTA, and quantizes from the registers: no second read.  Eight lanes hold a group of 128,
+// two 16-byte chunks each, 64 elements apart so that the lanes of a load are neighbours; products run
+// on pairs (f32x2).  Before, 16 lanes held a group, with one chunk each and scalar products: the
+// shuffles, scale bytes and scalar products of twice as many lanes cost 56.9 us for 16384 x 3072 with
+// residual (now 55.3) and 80.2 us for 4608 x 12288 (now 63.9).  Forming h gamma and the maxima before
+// the CTA's sum is known saves work behind the barrier but keeps twice the registers: 60.2 and 66.5 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -20,42 +23,59 @@ namespace svdq {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-// A thread keeps up to 8 chunks of 16 bytes in registers; with 8, of 256 threads at most.
-constexpr int max_threads(int vpt) { return vpt == 8 ? 256 : kMaxThreads; }
 
+// bf16(a + b) of 8 elements
 __device__ __forceinline__ uint4 add_bf16x8(uint4 a, uint4 b) {
   uint32_t x[4] = {a.x, a.y, a.z, a.w};
   const uint32_t y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(bf16x2_lo(x[i]) + bf16x2_lo(y[i]), bf16x2_hi(x[i]) + bf16x2_hi(y[i]));
+    const float2 f = __fadd2_rn(make_float2(bf16x2_lo(x[i]), bf16x2_hi(x[i])), make_float2(bf16x2_lo(y[i]), bf16x2_hi(y[i])));
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
     x[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
-__device__ __forceinline__ float sumsq8(uint4 v, float s) {
-  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+// s + the squares of 8 elements, in two sums
+__device__ __forceinline__ float2 sumsq8(uint4 h, float2 s) {
+  const uint32_t x[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    s = fmaf(bf16x2_lo(x[i]), bf16x2_lo(x[i]), s);
-    s = fmaf(bf16x2_hi(x[i]), bf16x2_hi(x[i]), s);
+    const float2 f = make_float2(bf16x2_lo(x[i]), bf16x2_hi(x[i]));
+    s = __ffma2_rn(f, f, s);
   }
   return s;
 }
-// y = (h * rstd) * gamma of one chunk; gamma is read through the read-only path (every row reads it)
-__device__ __forceinline__ void normed8(uint4 v, float rstd, const float* gamma, int c, float (&y)[8]) {
-  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+// y = (h rstd) gamma of 8 elements (gamma NULL: 1); returns max|y|.
+__device__ __forceinline__ float normed8(uint4 h, float rstd, const float* gamma, float2 (&y)[4]) {
+  const uint32_t x[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    y[i] = __fmul2_rn(make_float2(bf16x2_lo(x[i]), bf16x2_hi(x[i])), make_float2(rstd, rstd));
+  if (gamma) {       // through the read-only path: every row reads it
+    const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma)), g1 = __ldg(reinterpret_cast<const float4*>(gamma) + 1);
+    y[0] = __fmul2_rn(y[0], make_float2(g0.x, g0.y));
+    y[1] = __fmul2_rn(y[1], make_float2(g0.z, g0.w));
+    y[2] = __fmul2_rn(y[2], make_float2(g1.x, g1.y));
+    y[3] = __fmul2_rn(y[3], make_float2(g1.z, g1.w));
+  }
+  return fmaxf(fmaxf(fmaxf(fabsf(y[0].x), fabsf(y[0].y)), fmaxf(fabsf(y[1].x), fabsf(y[1].y))),
+               fmaxf(fmaxf(fabsf(y[2].x), fabsf(y[2].y)), fmaxf(fabsf(y[3].x), fabsf(y[3].y))));
+}
+__device__ __forceinline__ uint2 codes8(const float2 (&y)[4], float inv) {
+  uint32_t q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    y[2 * i] = bf16x2_lo(x[i]) * rstd;
-    y[2 * i + 1] = bf16x2_hi(x[i]) * rstd;
+    const float2 v = __fmul2_rn(y[i], make_float2(inv, inv));
+    q[i] = ptx::cvt_e4m3x2(v.x, v.y);
   }
-  if (gamma) {
-    const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma) + 2 * c);
-    const float4 g1 = __ldg(reinterpret_cast<const float4*>(gamma) + 2 * c + 1);
-    y[0] *= g0.x; y[1] *= g0.y; y[2] *= g0.z; y[3] *= g0.w;
-    y[4] *= g1.x; y[5] *= g1.y; y[6] *= g1.z; y[7] *= g1.w;
-  }
+  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+}
+// Maximum over the 8 lanes that hold one group.
+__device__ __forceinline__ float group_max8(float a) {
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
 }
 // Sum over the CTA, the same value in every thread; the order is fixed by the launch shape.
 __device__ __forceinline__ float cta_sum(float s) {
@@ -71,11 +91,12 @@ __device__ __forceinline__ float cta_sum(float s) {
   return s;
 }
 
-// VPT > 0: the row in registers, chunk c = threadIdx.x + i * blockDim.x.  VPT == 0: rows wider than
-// the registers of a CTA; a second pass reads h again (from H where it was written, since H may
-// have replaced an input).
+// VPT > 0: the row in registers; thread t has units t + i * blockDim.x, a unit being 16 elements of a
+// group (8 at its column and 8 at 64 further).  VPT == 0: rows wider than the registers of a CTA; a
+// second pass reads h again (from H where it was written, since H may have replaced an input).
 template <int VPT>
-__global__ void __launch_bounds__(max_threads(VPT)) rmsnorm_quant_kernel(NormParams p) {
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(NormParams p) {
+  constexpr int V = VPT > 0 ? VPT : 1;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int row = static_cast<int>(blockIdx.x);
@@ -84,74 +105,89 @@ __global__ void __launch_bounds__(max_threads(VPT)) rmsnorm_quant_kernel(NormPar
     fp8_zero_padding(p.scales, p.M, p.K, p.sfb, t, T);
     return;
   }
-  const int nc = p.K >> 3;
+  const int G = p.K >> 7, units = G * 8;
   const __nv_bfloat16* x = p.X + static_cast<size_t>(row) * p.ldx;
   const __nv_bfloat16* r = p.R ? p.R + static_cast<size_t>(row) * p.ldr : nullptr;
   __nv_bfloat16* hout = p.H ? p.H + static_cast<size_t>(row) * p.ldh : nullptr;
-  const size_t nscale = static_cast<size_t>((p.M + 127) / 128 * 128) * 4 * p.sfb;
+  uint8_t* codes = p.codes + static_cast<size_t>(row) * p.K;
   // padding groups of this row
-  if (t < 4 * p.sfb - (p.K >> 7)) p.scales[fp8_sf_offset(row, (p.K >> 7) + t, p.sfb)] = 0;
-  float s = 0.f;
-  uint4 h[VPT > 0 ? VPT : 1];
+  if (t < 4 * p.sfb - G) p.scales[fp8_sf_offset(row, G + t, p.sfb)] = 0;
+  auto column = [](int u) { return (u >> 3) * 128 + (u & 7) * 8; };
+  // h of one unit of the row, from the inputs
+  auto load = [&](int u, uint4 (&h)[2]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) h[q] = u < units ? ld_global_v4_na(x + column(u) + 64 * q) : make_uint4(0, 0, 0, 0);
+  };
+  auto add = [&](int u, uint4 (&h)[2], const uint4 (&rr)[2]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      h[q] = add_bf16x8(h[q], rr[q]);
+      if (hout && u < units) *reinterpret_cast<uint4*>(hout + column(u) + 64 * q) = h[q];
+    }
+  };
+  auto load_residual = [&](int u, uint4 (&rr)[2]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) rr[q] = u < units ? ld_global_v4_na(r + column(u) + 64 * q) : make_uint4(0, 0, 0, 0);
+  };
+  // norm, codes and scale of one unit; all lanes of the warp call it
+  auto quantize = [&](int u, const uint4 (&h)[2], float rstd) {
+    const bool on = u < units;
+    const float* g = on && p.gamma ? p.gamma + column(u) : nullptr;
+    float2 y[2][4];
+    float a = normed8(h[0], rstd, g, y[0]);
+    a = group_max8(fmaxf(a, normed8(h[1], rstd, g ? g + 64 : nullptr, y[1])));
+    const uint32_t b = fp8_scale_byte(a);
+    const float inv = fp8_inv_scale(b);
+    if (on && SVDQ_IN_GLOBAL(column(u) + 72 <= p.K, p.err)) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) *reinterpret_cast<uint2*>(codes + column(u) + 64 * q) = codes8(y[q], inv);
+      if ((u & 7) == 0) p.scales[fp8_sf_offset(row, u >> 3, p.sfb)] = static_cast<uint8_t>(b);
+    }
+  };
+  float2 s2 = make_float2(0.f, 0.f);
+  uint4 h[V][2];
   if (VPT > 0) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = t + i * T;
-      h[i] = c < nc ? ld_global_v4_na(x + static_cast<size_t>(c) * 8) : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < V; ++i) load(t + i * T, h[i]);
     if (r) {
-      uint4 rr[VPT > 0 ? VPT : 1];
+      uint4 rr[V][2];
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = t + i * T;
-        rr[i] = c < nc ? ld_global_v4_na(r + static_cast<size_t>(c) * 8) : make_uint4(0, 0, 0, 0);
-      }
+      for (int i = 0; i < V; ++i) load_residual(t + i * T, rr[i]);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = t + i * T;
-        h[i] = add_bf16x8(h[i], rr[i]);
-        if (hout && c < nc) *reinterpret_cast<uint4*>(hout + static_cast<size_t>(c) * 8) = h[i];
-      }
+      for (int i = 0; i < V; ++i) add(t + i * T, h[i], rr[i]);
     }
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) s = sumsq8(h[i], s);
+    for (int i = 0; i < V; ++i) s2 = sumsq8(h[i][1], sumsq8(h[i][0], s2));
   } else {
-    for (int c = t; c < nc; c += T) {
-      uint4 v = ld_global_v4_na(x + static_cast<size_t>(c) * 8);
+    for (int u = t; u < units; u += T) {
+      load(u, h[0]);
       if (r) {
-        v = add_bf16x8(v, ld_global_v4_na(r + static_cast<size_t>(c) * 8));
-        if (hout) *reinterpret_cast<uint4*>(hout + static_cast<size_t>(c) * 8) = v;
+        uint4 rr[2];
+        load_residual(u, rr);
+        add(u, h[0], rr);
       }
-      s = sumsq8(v, s);
+      s2 = sumsq8(h[0][1], sumsq8(h[0][0], s2));
     }
   }
-  s = cta_sum(s);
-  const float rstd = __frsqrt_rn(s / static_cast<float>(p.K) + p.eps);
+  const float rstd = __frsqrt_rn(cta_sum(s2.x + s2.y) / static_cast<float>(p.K) + p.eps);
   if (VPT > 0) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = t + i * T;
-      const bool on = c < nc;
-      float y[8];
-      normed8(h[i], rstd, on ? p.gamma : nullptr, c, y);
-      fp8_store_chunk(y, on, row, c, p.K, p.sfb, p.codes, p.scales, nscale, p.err);
-    }
+    for (int i = 0; i < V; ++i) quantize(t + i * T, h[i], rstd);
   } else {
-    for (int c0 = 0; c0 < nc; c0 += T) {
-      const int c = c0 + t;
-      const bool on = c < nc;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (on) {
-        if (hout) {
-          v = ld_global_v4_na(hout + static_cast<size_t>(c) * 8);
-        } else {
-          v = ld_global_v4_na(x + static_cast<size_t>(c) * 8);
-          if (r) v = add_bf16x8(v, ld_global_v4_na(r + static_cast<size_t>(c) * 8));
+    for (int u0 = 0; u0 < units; u0 += T) {
+      const int u = u0 + t;
+      if (hout) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) h[0][q] = u < units ? ld_global_v4_na(hout + column(u) + 64 * q) : make_uint4(0, 0, 0, 0);
+      } else {
+        load(u, h[0]);
+        if (r) {
+          uint4 rr[2];
+          load_residual(u, rr);
+          add(u, h[0], rr);
         }
       }
-      float y[8];
-      normed8(v, rstd, on ? p.gamma : nullptr, c, y);
-      fp8_store_chunk(y, on, row, c, p.K, p.sfb, p.codes, p.scales, nscale, p.err);
+      quantize(u, h[0], rstd);
     }
   }
 }
@@ -159,20 +195,14 @@ __global__ void __launch_bounds__(max_threads(VPT)) rmsnorm_quant_kernel(NormPar
 }  // namespace
 
 cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s) {
-  // About 192 threads a row when there are rows for every SM several times over (16384 x 3072 with
-  // residual: 56 us with 192 threads, 66 with 384; 4608 x 12288: see the header), one chunk per
-  // thread, up to 1024, when a row's latency is all that counts (one row: 1.9 us against 2.2).
-  const int nc = p.K / 8;
-  const int want = p.M >= 1024 ? 192 : kMaxThreads;
-  int vpt = 0, t = 0;
-  for (int v : {1, 2, 3, 4, 8}) {
-    const int need = (nc + v - 1) / v;
-    if (need > max_threads(v)) continue;
-    vpt = v;
-    t = need;
-    if (need <= want) break;
-  }
-  const int threads = vpt > 0 ? (t + 31) / 32 * 32 : kMaxThreads;
+  // With rows for every SM several times over, one unit per thread up to 256 threads, then two: with
+  // residual, 16384 x 3072 takes 55.3 us with 192 threads and 56.5 with 96, 8000 x 5120 47.7 us with 160
+  // and 50.1 with 320, 4608 x 12288 63.9 us with 384 and 69.9 with 192 (four units).  One unit, up to
+  // 1024 threads, where there are few rows and a row's latency is all that counts.
+  const int units = p.K / 16;
+  int vpt = units <= (p.M >= 1024 ? 256 : kMaxThreads) ? 1 : 2;
+  if ((units + vpt - 1) / vpt > kMaxThreads) vpt = 0;
+  const int threads = vpt > 0 ? ((units + vpt - 1) / vpt + 31) / 32 * 32 : kMaxThreads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.M) + (p.M % 128 ? 1u : 0u), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -184,10 +214,7 @@ cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   cudaError_t e = vpt == 0   ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<0>, p)
                   : vpt == 1 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<1>, p)
-                  : vpt == 2 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<2>, p)
-                  : vpt == 3 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<3>, p)
-                  : vpt == 4 ? cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<4>, p)
-                             : cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<8>, p);
+                             : cudaLaunchKernelEx(&cfg, rmsnorm_quant_kernel<2>, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
