@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
   const bool on = grp < G;
   const int row_end = min(p.M, row0 + kRows * ITERS);
   const size_t col = static_cast<size_t>(grp) * 128 + (t & 7) * 8;     // and col + 64
+  const int nsc = grp == G - 1 ? 4 * p.sfb - grp : 1;                  // scale bytes that its lanes write
   uint4 g[kRows][2], u[GATED ? kRows : 1][2];
   auto load = [&](int r) {
 #pragma unroll
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
     // y of every row, and the scale byte that this thread's own elements need.  The byte grows with the
     // absolute value, so the group's byte is the largest of its lanes': two rows' bytes go through one
     // shuffle as 16-bit halves.
-    float2 y[kRows][8];
+    float2 y[kRows][2][4];
     float amax[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) amax[i] = 0.f;
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
             v = __fmul2_rn(v, make_float2(bf16x2_lo(ux[e]), bf16x2_hi(ux[e])));
           }
           amax[i] = fmaxf(amax[i], fmaxf(fabsf(v.x), fabsf(v.y)));
-          y[i][4 * h + e] = v;
+          y[i][h][e] = v;
         }
       }
     }
@@ -131,28 +132,22 @@ __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
 #pragma unroll
       for (int o = 1; o <= 4; o <<= 1) sb[i] = max_u16x2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
     }
+    uint8_t* sc = p.scales + fp8_sf_offset(r, grp, p.sfb);      // r is even: the next row's is 16 bytes on
+    uint8_t* dst = p.codes + static_cast<size_t>(r) * p.K + col;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       if (i >= rows || !on) break;
-      const int row = r + i;
       const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
       const float inv = fp8_inv_scale(b);
-      uint8_t* dst = p.codes + static_cast<size_t>(row) * p.K + col;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = __fmul2_rn(y[i][4 * h + e], make_float2(inv, inv));
-          q[e] = ptx::cvt_e4m3x2(v.x, v.y);
-        }
         if (SVDQ_IN_GLOBAL(col + 64 * h + 8 <= static_cast<size_t>(p.K), p.err))
-          *reinterpret_cast<uint2*>(dst + 64 * h) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+          *reinterpret_cast<uint2*>(dst + 64 * h) = fp8_codes8(y[i][h], inv);
       }
-      if ((t & 7) == 0) p.scales[fp8_sf_offset(row, grp, p.sfb)] = static_cast<uint8_t>(b);
-      // the row's padding groups, by the lanes of its last group
-      if (grp == G - 1 && (t & 7) > 0 && (t & 7) < 4 * p.sfb - G + 1)
-        p.scales[fp8_sf_offset(row, G - 1 + (t & 7), p.sfb)] = 0;
+      dst += p.K;
+      // lane 0 has the group's byte; behind the row's last group the next lanes have the padding groups, up
+      // to the next multiple of four, which is the same 4-byte word
+      if ((t & 7) < nsc) sc[16 * i + (t & 7)] = (t & 7) == 0 ? static_cast<uint8_t>(b) : 0;
     }
   }
 }

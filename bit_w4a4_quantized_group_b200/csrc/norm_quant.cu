@@ -62,15 +62,6 @@ __device__ __forceinline__ float normed8(uint4 h, float rstd, const float* gamma
   return fmaxf(fmaxf(fmaxf(fabsf(y[0].x), fabsf(y[0].y)), fmaxf(fabsf(y[1].x), fabsf(y[1].y))),
                fmaxf(fmaxf(fabsf(y[2].x), fabsf(y[2].y)), fmaxf(fabsf(y[3].x), fabsf(y[3].y))));
 }
-__device__ __forceinline__ uint2 codes8(const float2 (&y)[4], float inv) {
-  uint32_t q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = __fmul2_rn(y[i], make_float2(inv, inv));
-    q[i] = ptx::cvt_e4m3x2(v.x, v.y);
-  }
-  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-}
 // Maximum over the 8 lanes that hold one group.
 __device__ __forceinline__ float group_max8(float a) {
   a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
@@ -140,7 +131,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(NormParams p
     const float inv = fp8_inv_scale(b);
     if (on && SVDQ_IN_GLOBAL(column(u) + 72 <= p.K, p.err)) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) *reinterpret_cast<uint2*>(codes + column(u) + 64 * q) = codes8(y[q], inv);
+      for (int q = 0; q < 2; ++q) *reinterpret_cast<uint2*>(codes + column(u) + 64 * q) = fp8_codes8(y[q], inv);
       if ((u & 7) == 0) p.scales[fp8_sf_offset(row, u >> 3, p.sfb)] = static_cast<uint8_t>(b);
     }
   };

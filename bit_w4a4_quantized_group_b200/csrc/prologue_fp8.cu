@@ -67,22 +67,30 @@ __device__ __forceinline__ uint4 smooth8(uint4 v, const Divisors& d) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// The scale byte that 8 elements need by themselves (the group's is the largest of its lanes').
-__device__ __forceinline__ uint32_t byte_of8(uint4 v) {
-  auto abs2 = [](const uint32_t& w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
-  const __nv_bfloat162 m = __hmax2(__hmax2(abs2(v.x), abs2(v.y)), __hmax2(abs2(v.z), abs2(v.w)));
-  return fp8_scale_byte(fmaxf(__low2float(m), __high2float(m)));
+// The pair of largest magnitude of either half, with signs that mean nothing (a NaN gives way to a number).
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_abs8(uint4 v) {
+  return max_abs_bf16x2(max_abs_bf16x2(v.x, v.y), max_abs_bf16x2(v.z, v.w));
+}
+// Two rows' pairs a and b -> the bits of max|a| (low half) and max|b| (high half).  Bits of magnitudes
+// order like the numbers, so that the group's maximum may be taken on them, two rows at a time.
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) {
+  return max_u16x2(__byte_perm(a, b, 0x5410) & 0x7FFF7FFFu, __byte_perm(a, b, 0x7632) & 0x7FFF7FFFu);
+}
+// The two rows' scale bytes, as 16-bit halves: fp8_scale_byte on the upper half of an fp32.
+__device__ __forceinline__ uint32_t scale_bytes(uint32_t bits) {
+  return max_u16x2(((bits + 0x001F001Fu) >> 7) & 0x01FF01FFu, 0x00080008u) - 0x00080008u;
 }
 __device__ __forceinline__ uint2 codes8(uint4 v, uint32_t byte) {
-  const float inv = fp8_inv_scale(byte);
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t q[4];
+  float2 f[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = __fmul2_rn(make_float2(bf16x2_lo(w[e]), bf16x2_hi(w[e])), make_float2(inv, inv));
-    q[e] = ptx::cvt_e4m3x2(f.x, f.y);
-  }
-  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+  for (int e = 0; e < 4; ++e) f[e] = make_float2(bf16x2_lo(w[e]), bf16x2_hi(w[e]));
+  return fp8_codes8(f, fp8_inv_scale(byte));
 }
 
 // ------------------------------------------------------------------ without a branch
@@ -124,10 +132,10 @@ __global__ void __launch_bounds__(kQThreads) quantize_fp8_kernel(const __nv_bflo
   }
   uint32_t sb[kQRows / 2];
 #pragma unroll
-  for (int i = 0; i < kQRows; ++i) {
+  for (int i = 0; i < kQRows; i += 2) {
     v[i] = smooth8<LAM>(v[i], d);
-    const uint32_t b = byte_of8(v[i]);
-    sb[i / 2] = i & 1 ? sb[i / 2] | (b << 16) : b;
+    v[i + 1] = smooth8<LAM>(v[i + 1], d);
+    sb[i / 2] = max_bits(max_abs8(v[i]), max_abs8(v[i + 1]));
   }
 #pragma unroll
   for (int o = 1; o <= 8; o <<= 1) {
@@ -136,13 +144,19 @@ __global__ void __launch_bounds__(kQThreads) quantize_fp8_kernel(const __nv_bflo
   }
   if (!on) return;
 #pragma unroll
+  for (int i = 0; i < kQRows / 2; ++i) sb[i] = scale_bytes(sb[i]);
+  uint8_t* dst = p.codes + static_cast<size_t>(row0) * p.K + static_cast<size_t>(c) * 8;
+  // Lane 0 of a group has its byte; behind the row's last group the next lanes have the padding groups,
+  // up to the next multiple of four, which is the same 4-byte word.
+  const int grp = c >> 4, j = c & 15, nsc = grp == G - 1 ? 4 * sfb - grp : 1;
+  uint8_t* sc = scales + fp8_sf_offset(row0, grp, sfb) + j;        // row0 is a multiple of 4: 16 bytes a row
+#pragma unroll
   for (int i = 0; i < kQRows; ++i) {
     if (i >= rows) break;
     const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
-    if (SVDQ_IN_GLOBAL(c * 8 + 8 <= p.K, p.err))
-      *reinterpret_cast<uint2*>(p.codes + static_cast<size_t>(row0 + i) * p.K + static_cast<size_t>(c) * 8) = codes8(v[i], b);
-    if ((c & 15) == 0) scales[fp8_sf_offset(row0 + i, c >> 4, sfb)] = static_cast<uint8_t>(b);
-    if (c < 4 * sfb - G) scales[fp8_sf_offset(row0 + i, G + c, sfb)] = 0;       // padding groups (c < 3)
+    if (SVDQ_IN_GLOBAL(c * 8 + 8 <= p.K, p.err)) *reinterpret_cast<uint2*>(dst) = codes8(v[i], b);
+    dst += p.K;
+    if (j < nsc) sc[16 * i] = j == 0 ? static_cast<uint8_t>(b) : 0;
   }
 }
 
@@ -341,9 +355,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         uint8_t* at = at0 + i * 256 + (((c & 7) ^ ((r0 + 2 * i) & 7)) << 4);
         v[i] = smooth8<LAM>(v[i], d);
         if (LAM && SVDQ_IN_SMEM(smem_raw, at, 16, p.err)) *reinterpret_cast<uint4*>(at) = v[i];
-        const uint32_t b = byte_of8(v[i]);
-        sb[i / 2] = i & 1 ? sb[i / 2] | (b << 16) : b;
       }
+#pragma unroll
+      for (int i = 0; i < kR; i += 2) sb[i / 2] = max_bits(max_abs8(v[i]), max_abs8(v[i + 1]));
       // X_hat is in place: hand the stage to the MMA warp before the codes are formed
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -353,16 +367,20 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
         for (int i = 0; i < kR / 2; ++i) sb[i] = max_u16x2(sb[i], __shfl_xor_sync(0xffffffffu, sb[i], o));
       }
+#pragma unroll
+      for (int i = 0; i < kR / 2; ++i) sb[i] = scale_bytes(sb[i]);
       uint8_t* dst = p.codes + static_cast<size_t>(m0 + r0) * p.K + grp * 128 + c * 8;
+      // Lane 0 of a group has its byte, the next ones those of the padding groups behind the last group
+      // (the same 4-byte word).  A warp's rows are in one run of 32: 16 bytes a row.  Rows past M read as
+      // zeros and get byte 0.
+      const int nsc = grp == G - 1 ? 4 * sfb - grp : 1;
+      uint8_t* sc = scales + fp8_sf_offset(m0 + r0, grp, sfb) + c;
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
-        const int row = m0 + r0 + 2 * i;
         const uint32_t b = (sb[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
-        if (row < p.M && SVDQ_IN_GLOBAL(grp < G, p.err)) *reinterpret_cast<uint2*>(dst) = codes8(v[i], b);
+        if (m0 + r0 + 2 * i < p.M && SVDQ_IN_GLOBAL(grp < G, p.err)) *reinterpret_cast<uint2*>(dst) = codes8(v[i], b);
         dst += 2 * static_cast<size_t>(p.K);
-        // rows past M read as zeros and get byte 0
-        if (c == 0) scales[fp8_sf_offset(row, grp, sfb)] = static_cast<uint8_t>(b);
-        if (grp == G - 1 && c > 0 && grp + c < 4 * sfb) scales[fp8_sf_offset(row, grp + c, sfb)] = 0;
+        if (c < nsc) sc[32 * i] = c == 0 ? static_cast<uint8_t>(b) : 0;
       }
       s += 2;                                              // S >= 2
       if (s >= S) { s -= S; ph ^= 1u; }

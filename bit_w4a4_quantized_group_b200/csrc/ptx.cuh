@@ -243,6 +243,16 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out) : "f"(hi), "f"(lo));
   return static_cast<uint32_t>(out);
 }
+// Four floats -> four E4M3 bytes, a in the low ones; the second conversion merges into the first's register.
+__device__ __forceinline__ uint32_t cvt_e4m3x4(float2 a, float2 b) {
+  uint32_t out;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(out) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return out;
+}
 // Two E4M3 bytes (bits 0-7, 8-15) -> two floats (exact).
 __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t c) {
   uint32_t h2;
