@@ -14,7 +14,10 @@
 // neighbours) in each of kRows rows, all its loads in flight together.  The exponentials and
 // reciprocals (two per element, 16 a clock and SM) and the instruction issue are each busy about as
 // long as memory, so products run on pairs (f32x2), row overheads are spread over 16 elements, and
-// large ungated calls fetch a thread's next rows under the stores of the current ones.
+// large ungated calls fetch a thread's next rows under the stores of the current ones.  Two elements
+// share a reciprocal in gated calls without lambda (2304 x 12288: 23.3 us against 24.5); without gating the
+// branch costs more than it saves (GELU 4608 x 12288: 38.6 us against 34.1), and with lambda the products
+// may leave the range.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -48,6 +51,34 @@ __device__ __forceinline__ float rcp_approx(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {      // NaN if one of them is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// d = 1 / d for 8 elements.  PAIRED (all d >= 1 or NaN): 1 / (a b) once, times b and times a, where every
+// product is in range; a NaN or an exp beyond 2^100 among the eight takes the plain way, each by itself.
+template <bool PAIRED>
+__device__ __forceinline__ void reciprocals(float2 (&d)[4]) {
+  float m = 0.f;
+  float p[4];
+  if (PAIRED) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = d[e].x * d[e].y;
+    m = max_nan(max_nan(p[0], p[1]), max_nan(p[2], p[3]));
+  }
+  if (PAIRED && m < 0x1p100f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float r = rcp_approx(p[e]);
+      d[e] = make_float2(r * d[e].y, r * d[e].x);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = make_float2(rcp_approx(d[e].x), rcp_approx(d[e].y));
+  }
 }
 
 // ITERS row pairs per CTA, one after the other, the next pair's loads under the current one's stores.
@@ -108,13 +139,17 @@ __global__ void __launch_bounds__(kThreads) glu_quant_kernel(GluParams p) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const uint32_t gx[4] = {g[i][h].x, g[i][h].y, g[i][h].z, g[i][h].w};
+        float2 d[4];                                    // then its reciprocal
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 x = make_float2(bf16x2_lo(gx[e]), bf16x2_hi(gx[e]));
-          const float2 nt = neg_t_log2<ACT>(x);
-          float2 d = __fadd2_rn(make_float2(ex2_approx(nt.x), ex2_approx(nt.y)), make_float2(1.f, 1.f));
-          if (LAM) d = __fmul2_rn(d, lam[e]);           // one reciprocal serves both divides
-          float2 v = __fmul2_rn(x, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+          const float2 nt = neg_t_log2<ACT>(make_float2(bf16x2_lo(gx[e]), bf16x2_hi(gx[e])));
+          d[e] = __fadd2_rn(make_float2(ex2_approx(nt.x), ex2_approx(nt.y)), make_float2(1.f, 1.f));
+          if (LAM) d[e] = __fmul2_rn(d[e], lam[e]);     // one reciprocal serves both divides
+        }
+        reciprocals<GATED && !LAM>(d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float2 v = __fmul2_rn(make_float2(bf16x2_lo(gx[e]), bf16x2_hi(gx[e])), d[e]);
           if (GATED) {
             const uint32_t ux[4] = {u[i][h].x, u[i][h].y, u[i][h].z, u[i][h].w};
             v = __fmul2_rn(v, make_float2(bf16x2_lo(ux[e]), bf16x2_hi(ux[e])));
@@ -166,10 +201,10 @@ cudaError_t launch(const GluParams& p, int iters, const cudaLaunchConfig_t& cfg)
 
 cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s) {
   const int64_t cblocks = (p.K / 128 + kGroups - 1) / kGroups;
-  // Four row pairs per CTA where that still leaves 3000 CTAs, four rounds of the device (GELU 4608 x
-  // 12288: 36.6 us against 38.7; 1000 rows of a small K get slower).  With gating a
-  // pair has twice the loads, and the next pair's registers cost more than they give (2304 x 12288:
-  // 25.9 us against 24.4).
+  // Four row pairs per CTA where that still leaves 3000 CTAs, four rounds of the device (GELU with lambda,
+  // 4608 x 12288: 35.8 us, before that 38.7 against 36.6; 1000 rows of a small K get slower).  With gating a
+  // pair has twice the loads, and the next pair's registers cost more than they give (2304 x 12288, before
+  // the shared reciprocals: 25.9 us against 24.4).
   const int iters = !p.up && cblocks * ((static_cast<int64_t>(p.M) + 2 * kIters - 1) / (2 * kIters)) >= 3000 ? kIters : 1;
   const int64_t rows = kRows * iters;
   const int64_t grid = cblocks * ((p.M + rows - 1) / rows) + (p.M % 128 ? 1 : 0);

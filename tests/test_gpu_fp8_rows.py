@@ -228,6 +228,35 @@ def test_glu_over_the_whole_range(act):
     F.check_quantized(codes, sb, _glu64(act, gate, None, None), GLU_DELTA, GLU_FLOOR)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_glu_gated_beside_every_value(act):
+    """Gates over the whole range next to ordinary ones: neighbours share a reciprocal where they can."""
+    bits = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16)
+    x = bits.view(torch.bfloat16)
+    x = x[torch.isfinite(x) & (x.float().abs() <= 2.0 ** 60)]
+    x = x[: x.numel() // 4 * 4]
+    gate = _acts(x.numel() // 4, 512, 9)
+    up = _acts(x.numel() // 4, 512, 10)
+    gate[:, [3, 130, 300, 511]] = x.view(-1, 4)
+    up[:, [3, 130, 300, 511]] = 2.0 ** -60            # so that the neighbours set the scale
+    codes, sb = _run_glu(act, gate, up, None)
+    F.check_quantized(codes, sb, _glu64(act, gate, up, None), GLU_DELTA, GLU_FLOOR)
+
+
+@pytest.mark.parametrize("lam", [False, True])
+def test_glu_gated_nan_leaves_its_neighbours(lam):
+    M, K = 4, 384
+    gate, up = _acts(M, K, 1), _acts(M, K, 2)
+    lm = torch.linspace(0.5, 2.0, K, device="cuda") if lam else None
+    ref = gate.clone()
+    ref[1, 9], ref[2, 200] = 0.0, 0.0
+    gate[1, 9], gate[2, 200] = float("nan"), float("nan")
+    codes, sb = _run_glu("silu", gate, up, lm)
+    assert codes[1, 9] & 0x7F == 0x7F and codes[2, 200] & 0x7F == 0x7F
+    codes[1, 9], codes[2, 200] = 0, 0
+    F.check_quantized(codes, sb, _glu64("silu", ref, up, lm), GLU_DELTA, GLU_FLOOR)
+
+
 def test_glu_zero_rows_and_nan_stay_where_they_are():
     M, K = 6, 256
     gate, up = _acts(M, K, 1), _acts(M, K, 2)
