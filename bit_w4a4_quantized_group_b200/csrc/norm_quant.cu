@@ -9,7 +9,7 @@
 // two 16-byte chunks each, 64 elements apart so that the lanes of a load are neighbours; products run
 // on pairs (f32x2).  Before, 16 lanes held a group, with one chunk each and scalar products: the
 // shuffles, scale bytes and scalar products of twice as many lanes cost 56.9 us for 16384 x 3072 with
-// residual (now 55.3) and 80.2 us for 4608 x 12288 (now 63.9).  Forming h gamma and the maxima before
+// residual (now 54.9) and 80.2 us for 4608 x 12288 (now 64.3).  Forming h gamma and the maxima before
 // the CTA's sum is known saves work behind the barrier but keeps twice the registers: 60.2 and 66.5 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -36,15 +36,16 @@ __device__ __forceinline__ uint4 add_bf16x8(uint4 a, uint4 b) {
   }
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
-// s + the squares of 8 elements, in two sums
-__device__ __forceinline__ float2 sumsq8(uint4 h, float2 s) {
-  const uint32_t x[4] = {h.x, h.y, h.z, h.w};
+// Sum of the squares of 16 elements.
+__device__ __forceinline__ float sumsq16(const uint4 (&h)[2]) {
+  const uint32_t x[8] = {h[0].x, h[0].y, h[0].z, h[0].w, h[1].x, h[1].y, h[1].z, h[1].w};
+  float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const float2 f = make_float2(bf16x2_lo(x[i]), bf16x2_hi(x[i]));
     s = __ffma2_rn(f, f, s);
   }
-  return s;
+  return s.x + s.y;
 }
 // y = (h rstd) gamma of 8 elements (gamma NULL: 1); returns max|y|.
 __device__ __forceinline__ float normed8(uint4 h, float rstd, const float* gamma, float2 (&y)[4]) {
@@ -68,25 +69,34 @@ __device__ __forceinline__ float group_max8(float a) {
   a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
   return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
 }
-// Sum over the CTA, the same value in every thread; the order is fixed by the launch shape.
-__device__ __forceinline__ float cta_sum(float s) {
-  __shared__ float part[32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-  __syncthreads();
+// Sum over the CTA of V values per thread, the same in every thread.  A value's place in the tree is that of
+// its unit t + i * blockDim.x, whatever the number of threads: a row's sum does not depend on which launch
+// shape takes it.
+template <int V>
+__device__ __forceinline__ float cta_sum(float (&s)[V]) {
+  __shared__ float part[32 * V];
   const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
-  s = lane < nw ? part[lane] : 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+    if (lane == 0) part[(threadIdx.x >> 5) + i * nw] = s[i];
+  }
+  __syncthreads();
+  float a = lane < nw * V ? part[lane] : 0.f;
+  if (V > 1) a += lane + 32 < nw * V ? part[lane + 32] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  return a;
 }
 
 // VPT > 0: the row in registers; thread t has units t + i * blockDim.x, a unit being 16 elements of a
 // group (8 at its column and 8 at 64 further).  VPT == 0: rows wider than the registers of a CTA; a
 // second pass reads h again (from H where it was written, since H may have replaced an input).
+// Registers: a CTA of 1024 threads may have 64 a thread; 40 and 52 let more CTAs share an SM (4608 x 3072
+// takes 17.8 us with 40, 18.2 with 34 and 18.8 with 32; 4608 x 12288 64.6 us with 52, 76 with 58, 66 with 48).
 template <int VPT>
-__global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(NormParams p) {
+__global__ void __maxnreg__(VPT == 2 ? 52 : 40) rmsnorm_quant_kernel(NormParams p) {
   constexpr int V = VPT > 0 ? VPT : 1;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -135,7 +145,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(NormParams p
       if ((u & 7) == 0) p.scales[fp8_sf_offset(row, u >> 3, p.sfb)] = static_cast<uint8_t>(b);
     }
   };
-  float2 s2 = make_float2(0.f, 0.f);
+  float s[V];
   uint4 h[V][2];
   if (VPT > 0) {
 #pragma unroll
@@ -148,8 +158,9 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(NormParams p
       for (int i = 0; i < V; ++i) add(t + i * T, h[i], rr[i]);
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) s2 = sumsq8(h[i][1], sumsq8(h[i][0], s2));
+    for (int i = 0; i < V; ++i) s[i] = sumsq16(h[i]);
   } else {
+    s[0] = 0.f;
     for (int u = t; u < units; u += T) {
       load(u, h[0]);
       if (r) {
@@ -157,10 +168,10 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(NormParams p
         load_residual(u, rr);
         add(u, h[0], rr);
       }
-      s2 = sumsq8(h[0][1], sumsq8(h[0][0], s2));
+      s[0] += sumsq16(h[0]);
     }
   }
-  const float rstd = __frsqrt_rn(cta_sum(s2.x + s2.y) / static_cast<float>(p.K) + p.eps);
+  const float rstd = __frsqrt_rn(cta_sum(s) / static_cast<float>(p.K) + p.eps);
   if (VPT > 0) {
 #pragma unroll
     for (int i = 0; i < V; ++i) quantize(t + i * T, h[i], rstd);
@@ -186,12 +197,12 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_quant_kernel(NormParams p
 }  // namespace
 
 cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s) {
-  // With rows for every SM several times over, one unit per thread up to 256 threads, then two: with
-  // residual, 16384 x 3072 takes 55.3 us with 192 threads and 56.5 with 96, 8000 x 5120 47.7 us with 160
-  // and 50.1 with 320, 4608 x 12288 63.9 us with 384 and 69.9 with 192 (four units).  One unit, up to
-  // 1024 threads, where there are few rows and a row's latency is all that counts.
+  // One unit per thread up to 256 threads, then two: with residual, 16384 x 3072 takes 54.9 us with 192
+  // threads and 56.5 with 96, 8000 x 5120 47.7 us with 160 and 50.1 with 320, 4608 x 12288 64.3 us with 384
+  // and 69.9 with 192 (four units).  Below 1024 rows, where a row's latency counts, one unit on up to 1024
+  // threads (300 x 8192: 4.4 us against 5.6; 1000 x 8192: 11.5 against 13.2).
   const int units = p.K / 16;
-  int vpt = units <= (p.M >= 1024 ? 256 : kMaxThreads) ? 1 : 2;
+  int vpt = units <= (p.M < 1024 ? kMaxThreads : 256) ? 1 : 2;
   if ((units + vpt - 1) / vpt > kMaxThreads) vpt = 0;
   const int threads = vpt > 0 ? ((units + vpt - 1) / vpt + 31) / 32 * 32 : kMaxThreads;
   cudaLaunchConfig_t cfg = {};

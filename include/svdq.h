@@ -231,7 +231,8 @@ svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int64_t N, int
  * (same pointer, same row stride); other overlaps of an output with another buffer are outside
  * the contract.  H needs a residual.  gamma is fp32 [K]; the norm before a layer with smoothing
  * factors takes gamma / lambda.  eps must be positive, normal and finite.  The sum of squares
- * is kept in fp32: a row whose sum of squares exceeds its range is outside the contract.
+ * is kept in fp32: a row whose sum of squares exceeds its range is outside the contract.  A row's
+ * outputs do not depend on M or on the other rows, bit for bit.
  * The outputs feed svdq_w4a4_gemm_lowrank_up with rank 0.
  */
 svdq_status svdq_rmsnorm_quantize_act(svdq_format fmt, int64_t M, int64_t K,

@@ -3,10 +3,10 @@ in 64 bits.
 
 Tolerances: a value may be half an E4M3 step away from a y that differs from the exact one by at
 most delta relatively.  delta is the fp32 error of the formula, in units of 2^-24:
-  norm  a thread keeps two sums of at most 8 * 3 products each (16 elements a unit; up to two units,
-        three in the looping form with K <= 40960 as here), one addition joins them, then 5 + 5 tree
-        steps: at most 50; halved by the square root, plus the divide, the addition of eps, the root
-        and two products: 50 / 2 + 5 <= 32 = 2^5: 2^-19;
+  norm  16 elements' squares go through two sums of 8 and an addition, in the looping form up to three
+        such sums are added (K <= 40960 here), then 5 + 1 + 5 tree steps: at most 50; halved by the
+        square root, plus the divide, the addition of eps, the root and two products: 50 / 2 + 5
+        <= 32 = 2^5: 2^-19;
   glu   exp(-t) is 2^a of an argument with at most four roundings, |a| <= 127 wherever the result is
         not below 2^-110: ln 2 * 127 * 4 = 352 units, 4 more for the hardware's 2^a (2^-22), 2 for
         its reciprocal and 4 for the sum and the products: < 512 = 2^9: 2^-15; below that, 2^-110
@@ -89,13 +89,22 @@ def test_norm(M, K, residual):
 @pytest.mark.parametrize("M,K", [(1024, 128), (1100, 4096), (1025, 4224), (1061, 8192), (1024, 12416)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_norm_many_rows(M, K, residual):
-    """The launch shapes that need many rows: one unit of 16 elements per thread, and two for wide rows."""
+    """Many rows with both launch shapes: one unit of 16 elements per thread, and two for wide rows."""
     X = _acts(M, K, M + K)
     R = _acts(M, K, M + 5 * K) if residual else None
     gamma = torch.linspace(-1.5, 1.5, K, device="cuda")
     codes, sb = _run_norm(X, R, gamma, 1e-6, None)
     h = X if R is None else (X.float() + R.float()).to(torch.bfloat16)
     F.check_quantized(codes, sb, F.rmsnorm64(_f64(h), _f64(gamma), 1e-6), NORM_DELTA)
+
+
+@pytest.mark.parametrize("K", [3200, 6400, 16384])
+def test_norm_bytes_do_not_depend_on_the_batch(K):
+    X, R = _acts(1500, K, 41), _acts(1500, K, 42)
+    ref = _run_norm(X, R, None, 1e-6, None)
+    for lo, hi in ((0, 1), (700, 829), (1499, 1500), (100, 1400)):
+        part = _run_norm(X[lo: hi], R[lo: hi], None, 1e-6, None)
+        assert np.array_equal(part[0], ref[0][lo: hi]) and np.array_equal(part[1], ref[1][lo: hi])
 
 
 def test_norm_rows_are_independent_and_may_be_strided():
