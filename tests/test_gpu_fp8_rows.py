@@ -9,7 +9,8 @@ most delta relatively.  delta is the fp32 error of the formula, in units of 2^-2
         <= 32 = 2^5: 2^-19;
   glu   exp(-t) is 2^a of an argument with at most four roundings, |a| <= 127 wherever the result is
         not below 2^-110: ln 2 * 127 * 4 = 352 units, 4 more for the hardware's 2^a (2^-22), 2 for
-        its reciprocal and 4 for the sum and the products: < 512 = 2^9: 2^-15; below that, 2^-110
+        its reciprocal and 4 for the sum and the products, 2 more where two elements share a
+        reciprocal, 1 / a = b / (a b) (b's own error cancels): < 512 = 2^9: 2^-15; below that, 2^-110
         absolutely.
 """
 import numpy as np
