@@ -265,6 +265,7 @@ def _column_vector(t, K, dev, name):
 
 
 _f32 = None
+_bf16 = None
 
 
 def _float32():
@@ -275,10 +276,20 @@ def _float32():
     return _f32
 
 
+def _bfloat16():
+    global _bf16
+    if _bf16 is None:
+        import torch
+        _bf16 = torch.bfloat16
+    return _bf16
+
+
 def _first_matrix(t, name):
-    """(shape, type, device, row stride) of a call's first matrix, which must lie on the current CUDA
-    device: the library launches there."""
+    """(shape, type, device, row stride) of a call's first matrix: bf16, the one type that the row
+    operators read, and on the current CUDA device, where the library launches (checked by the caller)."""
     shape, dtype, dev = t.shape, t.dtype, t.get_device()
+    if dtype is not (_bf16 or _bfloat16()) or len(shape) != 2:
+        raise ValueError(f"{name}: expected bfloat16 [M, K], got {tuple(shape)} {dtype}")
     ld, step = t.stride()
     if step != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
