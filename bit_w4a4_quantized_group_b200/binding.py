@@ -2,7 +2,8 @@
 
 Every function keeps the name of the C entry point in ``include/svdq.h``.
 The ``*_t`` helpers take torch tensors and pass their data pointers and the
-current CUDA stream; they check nothing the library does not check itself.
+current CUDA stream.  Those of the prologue and the GEMM check nothing the library does not
+check itself; those of the row operators also compare types, shapes, devices and buffer sizes.
 Loading fails loudly when the library is missing: there is no fallback.
 """
 from __future__ import annotations
@@ -284,6 +285,31 @@ def _bfloat16():
     return _bf16
 
 
+_u8 = None
+
+
+def _uint8():
+    global _u8
+    if _u8 is None:
+        import torch
+        _u8 = torch.uint8
+    return _u8
+
+
+def _fp8_outputs(codes, scales, M, K, dev):
+    """Pointers of the buffers that a row operator writes: dense uint8 on that device, M K bytes for the
+    codes and ceil(M / 128) * 128 * ceil(K / 512) * 4 for the scales, or more."""
+    u8 = _u8 or _uint8()
+    if (codes.dtype is not u8 or codes.nbytes < M * K or codes.get_device() != dev or not codes.is_contiguous()
+            or scales.dtype is not u8 or scales.nbytes < (M + 127 >> 7) * (K + 511 >> 9) * 512
+            or scales.get_device() != dev or not scales.is_contiguous()):
+        raise ValueError(f"a_codes, a_scales: expected contiguous uint8 of at least {M * K} and "
+                         f"{(M + 127 >> 7) * (K + 511 >> 9) * 512} elements on device {dev}, got "
+                         f"{tuple(codes.shape)} {codes.dtype} on {codes.device} and {tuple(scales.shape)} "
+                         f"{scales.dtype} on {scales.device}")
+    return codes.data_ptr(), scales.data_ptr()
+
+
 def _first_matrix(t, name):
     """(shape, type, device, row stride) of a call's first matrix: bf16, the one type that the row
     operators read, and on the current CUDA device, where the library launches (checked by the caller)."""
@@ -298,7 +324,8 @@ def _first_matrix(t, name):
 
 def rmsnorm_quantize_act_t(fmt, X, residual, gamma, eps, H, a_codes, a_scales, stream=None):
     """Residual addition + RMS norm + quantization on torch tensors: X, residual, H bf16 [M, K] (rows
-    may be strided; residual and H may be None), gamma fp32 [K] or None."""
+    may be strided; residual and H may be None), gamma fp32 [K] or None.  a_codes and a_scales are dense
+    uint8, at least as long as svdq_buffer_sizes says."""
     shape, dtype, dev, ldx = _first_matrix(X, "X")
     r = h = None
     ldr = ldh = 0
@@ -308,16 +335,19 @@ def rmsnorm_quantize_act_t(fmt, X, residual, gamma, eps, H, a_codes, a_scales, s
         ldh, h = _row_ld(H, shape, dtype, dev, "H"), H.data_ptr()
     if dev < 0 or dev != _current_device():
         raise ValueError(f"expected tensors on the current CUDA device, got one on {X.device}")
+    M, K = shape
+    codes, scales = _fp8_outputs(a_codes, a_scales, M, K, dev)
     st = (_calls or _hot()).svdq_rmsnorm_quantize_act(
-        _fmt(fmt), shape[0], shape[1], X.data_ptr(), ldx, r, ldr, _column_vector(gamma, shape[1], dev, "gamma"), eps,
-        h, ldh, a_codes.data_ptr(), a_scales.data_ptr(), _stream() if stream is None else stream)
+        _fmt(fmt), M, K, X.data_ptr(), ldx, r, ldr, _column_vector(gamma, K, dev, "gamma"), eps, h, ldh, codes, scales,
+        _stream() if stream is None else stream)
     if st != SVDQ_OK:
         raise SvdqError(st, "svdq_rmsnorm_quantize_act")
 
 
 def glu_quantize_act_t(fmt, act, gate, up, lam, a_codes, a_scales, stream=None):
     """act(gate) [* up] [/ lam] + quantization on torch tensors: act "silu" or "gelu" (tanh form), gate
-    and up bf16 [M, K] (column slices of a wider tensor will do; up may be None), lam fp32 [K] or None."""
+    and up bf16 [M, K] (column slices of a wider tensor will do; up may be None), lam fp32 [K] or None.
+    a_codes and a_scales as in rmsnorm_quantize_act_t."""
     code = ACTIVATIONS[act]
     shape, dtype, dev, ldg = _first_matrix(gate, "gate")
     u, ldu = None, 0
@@ -325,8 +355,10 @@ def glu_quantize_act_t(fmt, act, gate, up, lam, a_codes, a_scales, stream=None):
         ldu, u = _row_ld(up, shape, dtype, dev, "up"), up.data_ptr()
     if dev < 0 or dev != _current_device():
         raise ValueError(f"expected tensors on the current CUDA device, got one on {gate.device}")
+    M, K = shape
+    codes, scales = _fp8_outputs(a_codes, a_scales, M, K, dev)
     st = (_calls or _hot()).svdq_glu_quantize_act(
-        _fmt(fmt), code, shape[0], shape[1], gate.data_ptr(), ldg, u, ldu,
-        _column_vector(lam, shape[1], dev, "lam"), a_codes.data_ptr(), a_scales.data_ptr(), _stream() if stream is None else stream)
+        _fmt(fmt), code, M, K, gate.data_ptr(), ldg, u, ldu, _column_vector(lam, K, dev, "lam"), codes, scales,
+        _stream() if stream is None else stream)
     if st != SVDQ_OK:
         raise SvdqError(st, "svdq_glu_quantize_act")

@@ -24,3 +24,61 @@ def test_row_helpers_read_bf16_alone(dtype):
         B.glu_quantize_act_t("fp8", "silu", X, X, None, buf, buf, 0)
     with pytest.raises(ValueError, match="bfloat16"):
         B.glu_quantize_act_t("fp8", "silu", X.to(torch.bfloat16)[0], None, None, buf, buf, 0)      # one row as a vector
+
+
+@pytest.fixture
+def no_launch(monkeypatch):
+    """Host tensors pass for those of the current device, and a call that gets as far as the library
+    fails the test."""
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                raise AssertionError(f"{name} was called")
+            return call
+    monkeypatch.setattr(B, "_calls", Library())
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: getattr(t, "_dev", 0))
+    monkeypatch.setattr(B, "_stream", lambda: 0)
+
+
+def _bytes(n, dtype=torch.uint8, dev=0):
+    t = torch.zeros(n, dtype=dtype)
+    t._dev = dev
+    return t
+
+
+_M, _K = 130, 640
+_CODES, _SCALES = _M * _K, 256 * 8
+_BAD_BUFFERS = {
+    "codes too short": (_bytes(_CODES - 1), _bytes(_SCALES)),
+    "scales without the padding rows": (_bytes(_CODES), _bytes(_M * 8)),
+    "scales without the padding groups": (_bytes(_CODES), _bytes(256 * 5)),
+    "codes of another type": (_bytes(_CODES, torch.int32), _bytes(_SCALES)),
+    "scales of another type": (_bytes(_CODES), _bytes(_SCALES, torch.float32)),
+    "codes not dense": (_bytes(2 * _CODES)[::2], _bytes(_SCALES)),
+    "scales repeated": (_bytes(_CODES), _bytes(1).expand(_SCALES)),
+    "codes on another device": (_bytes(_CODES, dev=1), _bytes(_SCALES)),
+    "scales on the host": (_bytes(_CODES), _bytes(_SCALES, dev=-1)),
+}
+
+
+@pytest.mark.parametrize("which", sorted(_BAD_BUFFERS))
+def test_row_helpers_refuse_buffers_that_do_not_hold_the_outputs(which, no_launch):
+    X = torch.zeros((_M, _K), dtype=torch.bfloat16)
+    codes, scales = _BAD_BUFFERS[which]
+    with pytest.raises(ValueError, match="a_codes, a_scales"):
+        B.rmsnorm_quantize_act_t("fp8", X, None, None, 1e-6, None, codes, scales)
+    with pytest.raises(ValueError, match="a_codes, a_scales"):
+        B.glu_quantize_act_t("fp8", "silu", X, X, None, codes, scales)
+
+
+def test_row_helpers_take_buffers_of_the_stated_size(no_launch):
+    X = torch.zeros((_M, _K), dtype=torch.bfloat16)
+    sz = B.svdq_buffer_sizes("fp8", _M, 128, _K, 0)
+    assert (sz.a_codes, sz.a_scales) == (_CODES, _SCALES)
+    for extra in (0, 64):
+        buf = _bytes(_CODES + extra), _bytes(_SCALES + extra)
+        with pytest.raises(AssertionError, match="was called"):
+            B.rmsnorm_quantize_act_t("fp8", X, None, None, 1e-6, None, *buf)
+        with pytest.raises(AssertionError, match="was called"):
+            B.glu_quantize_act_t("fp8", "silu", X, None, None, *buf)
