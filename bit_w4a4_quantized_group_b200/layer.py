@@ -85,6 +85,11 @@ class W4A4LowRankLinear:
                 raise B.SvdqError(st, f"layer forward (device wait site {site})")
         return Y
 
+    def _check_width(self, t: torch.Tensor, name: str):
+        """The workspace is sized by this layer's K: rows of another width would be written past its end."""
+        if t.ndim != 2 or t.shape[1] != self.K:
+            raise ValueError(f"{name}: expected [M, {self.K}], got {tuple(t.shape)}")
+
     def _check_fp8_feed(self, what: str):
         if self.fmt != "fp8" or self.rank != 0:
             raise ValueError(f"{what} feeds fp8 layers without a low-rank branch (this one: {self.fmt}, rank {self.rank})")
@@ -104,6 +109,7 @@ class W4A4LowRankLinear:
         self._check_fp8_feed("forward_normed")
         if gamma is None and self.lam is not None:
             raise ValueError("a layer with smoothing factors needs gamma from fold_gamma")
+        self._check_width(X, "X")
         M = X.shape[0]
         ws = self.workspace(M)
         B.rmsnorm_quantize_act_t(self.fmt, X, residual, gamma, eps, H, ws["a_codes"], ws["a_scales"])
@@ -115,6 +121,7 @@ class W4A4LowRankLinear:
         first one's output (fp8, rank 0).  act is "silu" or "gelu" (tanh form); gate and up may be
         column slices of one GEMM output."""
         self._check_fp8_feed("forward_activated")
+        self._check_width(gate, "gate")
         M = gate.shape[0]
         ws = self.workspace(M)
         B.glu_quantize_act_t(self.fmt, act, gate, up, self.lam, ws["a_codes"], ws["a_scales"])

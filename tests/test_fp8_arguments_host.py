@@ -82,3 +82,31 @@ def test_row_helpers_take_buffers_of_the_stated_size(no_launch):
             B.rmsnorm_quantize_act_t("fp8", X, None, None, 1e-6, None, *buf)
         with pytest.raises(AssertionError, match="was called"):
             B.glu_quantize_act_t("fp8", "silu", X, None, None, *buf)
+
+
+def _layer(N, K):
+    import numpy as np
+    from bit_w4a4_quantized_group_b200 import prepare as P
+    from bit_w4a4_quantized_group_b200.layer import W4A4LowRankLinear
+    rng = np.random.default_rng(0)
+    prep = {"R_nk": rng.standard_normal((N, K)).astype(np.float32), "L1_rk": np.zeros((0, K), np.float32),
+            "L2_nr": np.zeros((N, 0), np.float32), "act_gscale": 1.0}
+    return W4A4LowRankLinear("fp8", N, K, P.pack("fp8", prep), None, 1.0, device="cpu")
+
+
+@pytest.mark.parametrize("width", [512, 128, 384])
+def test_layer_is_fed_rows_of_its_own_width(width, no_launch):
+    """A layer without smoothing has no [K] vector that would show it: the unsliced output of a
+    gate-up layer (512 here) once went into a workspace of half its size."""
+    lin = _layer(128, 256)
+    X = torch.zeros((4, width), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match=r"\[M, 256\]"):
+        lin.forward_activated("silu", X)
+    with pytest.raises(ValueError, match=r"\[M, 256\]"):
+        lin.forward_activated("silu", X, X)
+    with pytest.raises(ValueError, match=r"\[M, 256\]"):
+        lin.forward_normed(X, None, None)
+    with pytest.raises(ValueError, match=r"\[M, 256\]"):
+        lin.forward_normed(X, X, torch.ones(width), 1e-6, X)
+    with pytest.raises(ValueError, match=r"\[M, 256\]"):
+        lin.forward_normed(X[:, :64].reshape(256), None, None)
