@@ -28,6 +28,7 @@ class W4A4LowRankLinear:
         self.rank = packed["L1_bf16"].shape[0]
         self.w_codes = torch.from_numpy(packed["w_codes"]).to(self.device)
         self.w_scales = torch.from_numpy(packed["w_scales"]).to(self.device)
+        self._dev = self.w_codes.get_device()
         self.w_gscale = float(packed["w_gscale"])
         self.act_gscale = float(act_gscale)
         self.L1 = _to_dev_u16_as_bf16(packed["L1_bf16"], self.device) if self.rank else None
@@ -69,10 +70,9 @@ class W4A4LowRankLinear:
         returning it.  Without it, callers that need the guarantee poll
         ``binding.svdq_get_last_device_error`` themselves.
         """
-        M, K = X.shape
+        M, K = self._input_rows(X), self.K
+        Y = self._output(M, Y)
         ws = self.workspace(M)
-        if Y is None:
-            Y = torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device)
         stream = torch.cuda.current_stream(self.device).cuda_stream     # one lookup for both calls
         B.quantize_act_lowrank_down_t(self.fmt, X, self.lam, self.act_gscale, self.L1,
                                       ws["a_codes"], ws["a_scales"], ws["Z"], stream)
@@ -83,6 +83,25 @@ class W4A4LowRankLinear:
             st, site = B.svdq_get_last_device_error(torch.cuda.current_stream(self.device).cuda_stream)
             if st != B.SVDQ_OK:
                 raise B.SvdqError(st, f"layer forward (device wait site {site})")
+        return Y
+
+    def _input_rows(self, X: torch.Tensor) -> int:
+        """M of a prologue's input, which the library reads as dense bf16 [M, K] on the current device."""
+        if X.ndim != 2 or X.shape[1] != self.K or X.dtype is not torch.bfloat16 or not X.is_contiguous():
+            raise ValueError(f"X: expected contiguous bfloat16 [M, {self.K}], got {tuple(X.shape)} {X.dtype}, "
+                             f"strides {X.stride()}")
+        if self._dev < 0 or X.get_device() != self._dev or B._current_device() != self._dev:
+            raise ValueError(f"X on {X.device}: it and the layer (on {self.w_codes.device}) have to lie on the "
+                             "current CUDA device")
+        return X.shape[0]
+
+    def _output(self, M: int, Y: Optional[torch.Tensor]) -> torch.Tensor:
+        """Y for M rows: a new tensor, or the caller's, which the GEMM writes as dense bf16 [M, N]."""
+        if Y is None:
+            return torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device)
+        if Y.dtype is not torch.bfloat16 or Y.nbytes < 2 * M * self.N or not Y.is_contiguous() or Y.get_device() != self._dev:
+            raise ValueError(f"Y: expected contiguous bfloat16 [{M}, {self.N}] on {self.w_codes.device}, got "
+                             f"{tuple(Y.shape)} {Y.dtype}, strides {Y.stride()}, on {Y.device}")
         return Y
 
     def _check_width(self, t: torch.Tensor, name: str):
@@ -111,9 +130,11 @@ class W4A4LowRankLinear:
             raise ValueError("a layer with smoothing factors needs gamma from fold_gamma")
         self._check_width(X, "X")
         M = X.shape[0]
+        Y = self._output(M, Y)
         ws = self.workspace(M)
         B.rmsnorm_quantize_act_t(self.fmt, X, residual, gamma, eps, H, ws["a_codes"], ws["a_scales"])
-        return self._gemm(M, Y)
+        self._gemm(M, Y)
+        return Y
 
     def forward_activated(self, act: str, gate: torch.Tensor, up: Optional[torch.Tensor] = None,
                           Y: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -123,18 +144,19 @@ class W4A4LowRankLinear:
         self._check_fp8_feed("forward_activated")
         self._check_width(gate, "gate")
         M = gate.shape[0]
+        Y = self._output(M, Y)
         ws = self.workspace(M)
         B.glu_quantize_act_t(self.fmt, act, gate, up, self.lam, ws["a_codes"], ws["a_scales"])
-        return self._gemm(M, Y)
-
-    def _gemm(self, M: int, Y: Optional[torch.Tensor]) -> torch.Tensor:
-        if Y is None:
-            Y = torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device)
-        self.gemm_only(M, Y)
+        self._gemm(M, Y)
         return Y
 
     def gemm_only(self, M: int, Y: torch.Tensor, rank: Optional[int] = None):
         """The fused GEMM alone on the current workspace (rank 0 drops the branch)."""
+        if self._dev < 0 or B._current_device() != self._dev:
+            raise ValueError(f"the layer (on {self.w_codes.device}) has to lie on the current CUDA device")
+        self._gemm(M, self._output(M, Y), rank)
+
+    def _gemm(self, M: int, Y: torch.Tensor, rank: Optional[int] = None):
         ws = self.workspace(M)
         r = self.rank if rank is None else rank
         B.w4a4_gemm_lowrank_up_t(self.fmt, M, self.N, self.K, r, ws["a_codes"], ws["a_scales"],
@@ -143,7 +165,7 @@ class W4A4LowRankLinear:
 
     def prologue_only(self, X: torch.Tensor, rank: Optional[int] = None):
         """The prologue alone (rank 0 quantizes without the down projection)."""
-        M, _ = X.shape
+        M = self._input_rows(X)
         ws = self.workspace(M)
         r = self.rank if rank is None else rank
         B.quantize_act_lowrank_down_t(self.fmt, X, self.lam, self.act_gscale, self.L1 if r else None,

@@ -39,6 +39,7 @@ def no_launch(monkeypatch):
     monkeypatch.setattr(B, "_current_device", lambda: 0)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: getattr(t, "_dev", 0))
     monkeypatch.setattr(B, "_stream", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: type("Stream", (), {"cuda_stream": 0}))
 
 
 def _bytes(n, dtype=torch.uint8, dev=0):
@@ -110,3 +111,55 @@ def test_layer_is_fed_rows_of_its_own_width(width, no_launch):
         lin.forward_normed(X, X, torch.ones(width), 1e-6, X)
     with pytest.raises(ValueError, match=r"\[M, 256\]"):
         lin.forward_normed(X[:, :64].reshape(256), None, None)
+
+
+def _calls(lin, X, Y):
+    yield lambda: lin.forward(X, Y)
+    yield lambda: lin.forward_normed(X, None, None, Y=Y)
+    yield lambda: lin.forward_activated("silu", X, Y=Y)
+
+
+@pytest.mark.parametrize("case", ["short", "float32", "float16", "transposed", "column slice", "expanded", "host", "other device"])
+def test_layer_refuses_outputs_that_do_not_hold_its_result(case, no_launch):
+    lin = _layer(128, 256)
+    X = torch.zeros((4, 256), dtype=torch.bfloat16)
+    Y = torch.zeros((4, 128), dtype=torch.bfloat16)
+    bad = {"short": Y[:3], "float32": Y.float(), "float16": Y.half(), "transposed": torch.zeros((128, 4), dtype=torch.bfloat16).t(),
+           "column slice": torch.zeros((4, 256), dtype=torch.bfloat16)[:, :128], "expanded": Y[:1].expand(4, 128)}.get(case, Y)
+    if case in ("host", "other device"):
+        bad._dev = -1 if case == "host" else 1
+    for call in _calls(lin, X, bad):
+        with pytest.raises(ValueError, match="Y: expected"):
+            call()
+    with pytest.raises(ValueError, match="Y: expected"):
+        lin.gemm_only(4, bad)
+    for call in _calls(lin, X, torch.zeros((5, 128), dtype=torch.bfloat16)):      # more rows than needed are no fault
+        with pytest.raises(AssertionError, match="was called"):
+            call()
+
+
+@pytest.mark.parametrize("case", ["wide", "narrow", "float32", "float16", "transposed", "column slice", "one row as a vector"])
+def test_layer_forward_refuses_inputs_that_are_not_its_rows(case, no_launch):
+    lin = _layer(128, 256)
+    X = torch.zeros((4, 256), dtype=torch.bfloat16)
+    bad = {"wide": torch.zeros((4, 512), dtype=torch.bfloat16), "narrow": X[:, :128].contiguous(), "float32": X.float(),
+           "float16": X.half(), "transposed": torch.zeros((256, 4), dtype=torch.bfloat16).t(),
+           "column slice": torch.zeros((4, 512), dtype=torch.bfloat16)[:, :256], "one row as a vector": X[0]}[case]
+    for call in (lambda: lin.forward(bad), lambda: lin.prologue_only(bad)):
+        with pytest.raises(ValueError, match="X: expected"):
+            call()
+
+
+def test_layer_refuses_to_launch_on_another_device(no_launch, monkeypatch):
+    lin = _layer(128, 256)
+    X = torch.zeros((4, 256), dtype=torch.bfloat16)
+    Y = torch.zeros((4, 128), dtype=torch.bfloat16)
+    elsewhere = X.clone()
+    elsewhere._dev = 1
+    for call in (lambda: lin.forward(elsewhere), lambda: lin.prologue_only(elsewhere)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+    monkeypatch.setattr(B, "_current_device", lambda: 1)
+    for call in [*_calls(lin, X, Y), lambda: lin.prologue_only(X), lambda: lin.gemm_only(4, Y)]:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
