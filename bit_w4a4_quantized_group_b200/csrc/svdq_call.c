@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <stdint.h>
+#include <string.h>
 
 #include "svdq.h"
 
@@ -25,13 +26,29 @@ static fn_rmsnorm rmsnorm_fn;
 static fn_glu glu_fn;
 
 static int64_t as_int(PyObject* o) { return (int64_t)PyLong_AsLongLong(o); }
+/* What ctypes takes for a pointer besides an address and None: a c_void_p, or an object that names one,
+ * such as a torch.cuda.Stream. */
+static void* as_ptr_of_object(PyObject* o, int nested);
 static void* as_ptr(PyObject* o) {
   if (o == Py_None) return NULL;
-  if (!PyLong_Check(o)) {
-    PyErr_SetString(PyExc_TypeError, "expected an address or None");
-    return NULL;
+  if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
+  return as_ptr_of_object(o, 0);
+}
+static void* as_ptr_of_object(PyObject* o, int nested) {
+  if (PyErr_Occurred()) return NULL; /* an earlier argument's */
+  const char* dot = strrchr(Py_TYPE(o)->tp_name, '.');
+  const int is_pointer = strcmp(dot ? dot + 1 : Py_TYPE(o)->tp_name, "c_void_p") == 0;
+  PyObject* v = is_pointer || !nested ? PyObject_GetAttrString(o, is_pointer ? "value" : "_as_parameter_") : NULL;
+  void* p = NULL;
+  if (v && (v == Py_None || PyLong_Check(v))) {
+    p = v == Py_None ? NULL : PyLong_AsVoidPtr(v);
+  } else if (v && !nested) {
+    p = as_ptr_of_object(v, 1);
+  } else {
+    PyErr_SetString(PyExc_TypeError, "expected an address, a c_void_p or None");
   }
-  return PyLong_AsVoidPtr(o);
+  Py_XDECREF(v);
+  return p;
 }
 static float as_float(PyObject* o) { return (float)PyFloat_AsDouble(o); }
 

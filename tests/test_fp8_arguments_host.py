@@ -163,3 +163,26 @@ def test_layer_refuses_to_launch_on_another_device(no_launch, monkeypatch):
     for call in [*_calls(lin, X, Y), lambda: lin.prologue_only(X), lambda: lin.gemm_only(4, Y)]:
         with pytest.raises(ValueError, match="current CUDA device"):
             call()
+
+
+def test_hot_calls_take_the_streams_that_ctypes_takes():
+    """A stream may be a raw handle, None, a c_void_p, or an object with one (torch.cuda.Stream)."""
+    import ctypes
+
+    class Stream:
+        def __init__(self, p):
+            self._as_parameter_ = p
+
+    calls = {"svdq_glu_quantize_act": [5, 1, 0, 256, 1 << 20, 256, None, 0, None, 1 << 20, 1 << 20],     # M = 0: refused
+             "svdq_quantize_act_lowrank_down": [5, 0, 256, 0, 1 << 20, None, 1.0, None, 1 << 20, 1 << 20, None]}
+    for name, args in calls.items():
+        for fn in (getattr(B.load(), name), getattr(B._hot(), name)):
+            for stream in (None, 0, 1 << 40, ctypes.c_void_p(None), ctypes.c_void_p(1 << 40), Stream(ctypes.c_void_p(1 << 40)),
+                           Stream(1 << 40), Stream(ctypes.c_void_p(None))):
+                assert fn(*args, stream) == B.SVDQ_ERR_INVALID_ARG
+            for wrong in ("x", 1.5, ctypes.c_int(3), object(), Stream("x")):
+                if fn is getattr(B.load(), name) and isinstance(getattr(wrong, "_as_parameter_", wrong), str):
+                    continue                       # ctypes takes a text for the address of its characters
+                with pytest.raises((TypeError, ctypes.ArgumentError)):
+                    fn(*args, wrong)
+    assert isinstance(torch.cuda.Stream._as_parameter_, property)
