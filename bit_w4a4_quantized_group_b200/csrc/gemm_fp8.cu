@@ -215,16 +215,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < tiles.count && ok; ++j) {
         const int a = C::kAccs == 2 ? (j & 1) : 0;
         const uint32_t use = static_cast<uint32_t>(C::kAccs == 2 ? j >> 1 : j);
-        if (!wait_bounded(&sh->acc_empty[a], (use & 1u) ^ 1u, abort_flag, p.err, kErrSiteGemmAccEmpty)) break;
+        if (!wait_bounded_warp(&sh->acc_empty[a], (use & 1u) ^ 1u, abort_flag, p.err, kErrSiteGemmAccEmpty)) break;
         ptx::tc_fence_after();
         const uint32_t acc = tmem + static_cast<uint32_t>(a * BN);
         // a tile that starts inside a 128-row scale block (BN 64 and 192) skips the block's first columns
         const uint32_t sfb_skip = static_cast<uint32_t>((tiles.nb(j) * BN) & 127) / 32;
         for (int d = 0; d < nd + nk_lr; ++d) {
-          if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) { ok = false; break; }
+          if (!wait_bounded_warp(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) { ok = false; break; }
           const bool main_slot = d < nd;
           if (main_slot && d % kSfSlots == 0 &&
-              !wait_bounded(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) {
+              !wait_bounded_warp(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) {
             ok = false;
             break;
           }
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t sfdesc0 = ptx::sdesc_sf(ptx::smem_u32(sf_smem));
       const int blocks = tiles.count * ((nk + 3) / 4);
       for (int i = 0; i < blocks; ++i) {
-        if (!wait_bounded(&sh->sf_full[b], sfph, abort_flag, p.err, kErrSiteGemmFull)) break;
+        if (!wait_bounded_warp(&sh->sf_full[b], sfph, abort_flag, p.err, kErrSiteGemmFull)) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t sd = sfdesc0 + static_cast<uint64_t>(b) * (C::kSfBytes / 16);
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned short touch = __ldg(reinterpret_cast<const unsigned short*>(p.bias) + col0 + lane * 64);
         asm volatile("" ::"h"(touch));
       }
-      if (!wait_bounded(&sh->acc_full[a], use & 1u, abort_flag, p.err, kErrSiteGemmAccFull)) break;
+      if (!wait_bounded_warp(&sh->acc_full[a], use & 1u, abort_flag, p.err, kErrSiteGemmAccFull)) break;
       ptx::tc_fence_after();
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * BN + h * C::kColsPerWarp;
       const int row = m0 + q * 32 + lane;

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sfdesc0 = ptx::sdesc_sf(ptx::smem_u32(sf_smem));
     const int blocks = ((kb + nk - 1) >> 2) - (kb >> 2) + 1;
     for (int i = 0; i < blocks; ++i) {
-      if (!wait_bounded_call(&sh->sf_full[b], sfph, abort_flag, p.err, kErrSiteGemmFull)) break;
+      if (!wait_bounded_call_warp(&sh->sf_full[b], sfph, abort_flag, p.err, kErrSiteGemmFull)) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         const uint64_t sd = sfdesc0 + static_cast<uint64_t>(b) * (2 * kSfBlk / 16);
@@ -192,10 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem));
     const uint32_t sfx_skip = static_cast<uint32_t>(m0 & 127) / 32;    // T = 16 has m0 = 0
     for (int k = 0; k < nk + nk_lr; ++k) {
-      if (!wait_bounded_call(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) break;
+      if (!wait_bounded_call_warp(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) break;
       const bool main_step = k < nk;
       const uint32_t id = static_cast<uint32_t>((kb + k) & 3);
-      if (starts_block(k) && !wait_bounded_call(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) break;
+      if (starts_block(k) && !wait_bounded_call_warp(&sh->sf_ready[b], sfph, abort_flag, p.err, kErrSiteGemmSfReady)) break;
       ptx::tc_fence_after();
       const bool sf_done = main_step && (id == 3 || k == nk - 1);
       if (ptx::elect_one()) {
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     const int n = q * 32 + lane;
     if (ks > 1) ptx::cluster_wait();
-    if (wait_bounded_call(&sh->acc_full, 0u, abort_flag, p.err, kErrSiteGemmAccFull)) {
+    if (wait_bounded_call_warp(&sh->acc_full, 0u, abort_flag, p.err, kErrSiteGemmAccFull)) {
       ptx::tc_fence_after();
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
       float* part = reinterpret_cast<float*>(smem) + n;       // [token][128], in the drained ring
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();                                           // this CTA's own rows lie in its ring
   bool ok = *abort_flag == 0;
   if (ks > 1) {
-    ok = wait_bounded_call(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
+    ok = wait_bounded_call_warp(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
     // what the others sent has arrived; when all CTAs say so, every copy has left its source
     __syncwarp();
     ptx::cluster_arrive();

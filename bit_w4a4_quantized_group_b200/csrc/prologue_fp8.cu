@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) l[i] = __ldg(p.lam + gb * 128 + i * 32 + lane);
     for (int g = 0; g < ng; ++g) {
-      if (!wait_bounded(&sh->empty[s], ph, abort_flag, p.err, kErrSiteProEmpty)) break;
+      if (!wait_bounded_warp(&sh->empty[s], ph, abort_flag, p.err, kErrSiteProEmpty)) break;
       uint8_t* st = smem + s * stage;
       if (lane == 0) {
         ptx::mbar_expect_tx(&sh->full[s], kXBytes + 256u * rank);
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const uint32_t idesc = idesc_bf16p(kMmaRows, rank);
     const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem));
     for (int g = 0; g < ng; ++g) {
-      if (!wait_bounded(&sh->xh_full[s], ph, abort_flag, p.err, kErrSiteProPair)) break;
+      if (!wait_bounded_warp(&sh->xh_full[s], ph, abort_flag, p.err, kErrSiteProPair)) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         const uint64_t ad = desc0 + static_cast<uint64_t>(s) * (stage / 16);
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     int s = set % S;
     uint32_t ph = static_cast<uint32_t>(set / S) & 1u;
     for (int g = set; g < ng; g += 2) {
-      if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteProFull)) break;
+      if (!wait_bounded_warp(&sh->full[s], ph, abort_flag, p.err, kErrSiteProFull)) break;
       uint8_t* st = smem + s * stage;
       Divisors d;
       if (LAM) {
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       // ---------------------------------------------------------- Z: thread = row, column = rank index
       if (ks > 1) ptx::cluster_wait();
       float* part = reinterpret_cast<float*>(smem);          // [row][zrow], in the drained ring
-      if (wait_bounded(&sh->acc_full, 0u, abort_flag, p.err, kErrSiteGemmAccFull)) {
+      if (wait_bounded_warp(&sh->acc_full, 0u, abort_flag, p.err, kErrSiteGemmAccFull)) {
         ptx::tc_fence_after();
         const int row = warp * 32 + lane;
         const uint32_t base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   __syncthreads();
   bool ok = *abort_flag == 0;
   if (ks > 1) {
-    ok = wait_bounded(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
+    ok = wait_bounded_warp(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
     // what the others sent has arrived; when all CTAs say so, every copy has left its source
     __syncwarp();
     ptx::cluster_arrive();

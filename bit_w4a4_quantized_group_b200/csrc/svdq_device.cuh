@@ -30,6 +30,7 @@ enum : int {
   kErrSiteGemmConvDone = 19,
   kErrSiteGemmAccFinal = 20,
   kErrSiteSelftest = 90,
+  kErrSiteSelftestParted = 91,
   // Debug builds (-DSVDQ_DEBUG) only: an access outside its buffer was found and skipped.
   kErrSiteBoundsGlobal = 201,   // a plain global load or store past its buffer
   kErrSiteBoundsShared = 202,   // a shared-memory access past the dynamic allocation
@@ -99,6 +100,26 @@ static __device__ __noinline__ bool wait_bounded_loop(uint64_t* bar, uint32_t pa
 __device__ __forceinline__ bool wait_bounded_call(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
                                                   int site) {
   return ptx::mbar_try_wait(ptx::smem_u32(bar), parity) || wait_bounded_loop(bar, parity, abort_flag, err, site);
+}
+
+// wait_bounded by a whole converged warp, with one result for all its lanes.  Each lane polls for itself, so
+// a barrier that completes just as the limit runs out may let some lanes pass and not others; lanes that part
+// there would meet again in an elect.sync or an .aligned instruction that names the whole warp, and wait
+// without a limit.  The vote makes every lane give up when one has.
+// The first poll is voted on by itself: where every lane passes there, as nearly always, nothing branches.
+__device__ __forceinline__ bool wait_bounded_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                  int site, uint64_t limit_ns = kWaitLimitNs) {
+  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(ptx::smem_u32(bar), parity))) return true;
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err, site, limit_ns));
+}
+static __device__ __noinline__ bool wait_bounded_loop_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                           int* err, int site) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err, site));
+}
+__device__ __forceinline__ bool wait_bounded_call_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                       int* err, int site) {
+  return __all_sync(0xffffffffu, ptx::mbar_try_wait(ptx::smem_u32(bar), parity)) ||
+         wait_bounded_loop_warp(bar, parity, abort_flag, err, site);
 }
 
 // Tile schedule of the persistent pair GEMMs: cluster c takes the contiguous run

@@ -1,0 +1,50 @@
+"""A bounded wait that a whole warp makes has one result for all its lanes.  Lanes that part at a wait (one
+sees the barrier complete just as another's limit runs out) would meet again in instructions that name the
+whole warp and have no limit: elect.sync, warp barriers, .aligned forms.  Read from the kernels' sources:
+every wait is either the voting form or stands in a block that one lane runs, and a voting one never does."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_w4a4_quantized_group_b200", "csrc")
+
+
+def _waits(text):
+    """(line, name, whether one lane alone runs it) of every wait_bounded* call."""
+    text = re.sub(r"//[^\n]*", lambda m: " " * len(m.group()), text)
+    one_lane = []           # for each open brace: does its block run in one lane?
+    out = []
+    token = re.compile(r"\{|\}|\b(wait_bounded\w*)\s*\(")
+    for m in token.finditer(text):
+        if m.group() == "{":
+            head = text[max(text.rfind(c, 0, m.start()) for c in ";{}") + 1: m.start()]
+            alone = re.search(r"if \((?:[^()]* && )?(?:lane|threadIdx\.x) == 0\)\s*$", head) or re.search(
+                r"if \(ptx::elect_one\(\)\)\s*$", head)
+            one_lane.append(bool(alone) or (bool(one_lane) and one_lane[-1]))
+        elif m.group() == "}":
+            one_lane.pop()
+        else:
+            out.append((text.count("\n", 0, m.start()) + 1, m.group(1), bool(one_lane) and one_lane[-1]))
+    assert not one_lane
+    return out
+
+
+def test_the_reader_tells_one_lane_from_a_warp():
+    src = """
+    if (warp == 0) { if (lane == 0) { for (;;) { if (!wait_bounded(a)) break; } } __syncwarp(); }
+    else if (warp == 1) { if (wait_bounded_warp(b)) { } // if (lane == 0) {
+      wait_bounded(c); if (ok && lane == 0) { wait_bounded_call(d); } if (ptx::elect_one()) { wait_bounded_warp(e); } }
+    """
+    assert [(n, alone) for _, n, alone in _waits(src)] == [
+        ("wait_bounded", True), ("wait_bounded_warp", False), ("wait_bounded", False), ("wait_bounded_call", True),
+        ("wait_bounded_warp", True)]
+
+
+@pytest.mark.parametrize("name", ["gemm_fp8.cu", "gemm_fp8_small.cu", "prologue_fp8.cu"])
+def test_waits_of_whole_warps_are_voted_on(name):
+    with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+        waits = _waits(f.read())
+    assert waits
+    wrong = [(line, n) for line, n, alone in waits if n.endswith("_warp") == alone]
+    assert not wrong, f"{name}: {wrong}"
