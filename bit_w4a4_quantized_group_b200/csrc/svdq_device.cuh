@@ -136,8 +136,9 @@ struct TileSeq {
   __device__ int nb(int j) const { return (begin + j) % tiles_n; }
 };
 
-// Named barrier `id` over `count` threads (a multiple of 32).
+// Named barrier `id` over `count` threads (a multiple of 32), whole warps (an aligned form too).
 __device__ __forceinline__ void named_barrier_sync(int id, int count) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 

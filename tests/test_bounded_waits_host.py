@@ -48,3 +48,17 @@ def test_waits_of_whole_warps_are_voted_on(name):
     assert waits
     wrong = [(line, n) for line, n, alone in waits if n.endswith("_warp") == alone]
     assert not wrong, f"{name}: {wrong}"
+
+
+def test_barriers_in_aligned_form_gather_the_warp_first():
+    """barrier.cluster.*.aligned and bar.sync want all lanes of a warp; a role that branched by lane (a
+    producer whose lane 0 starts the copies) may reach them in parts unless it is gathered."""
+    found = 0
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r'asm volatile\(\s*"(barrier\.cluster[^"]*\.aligned|bar\.sync)', text):
+            body = text[text.rfind("{", 0, m.start()): m.start()]
+            assert "__syncwarp();" in body, (name, text.count("\n", 0, m.start()) + 1)
+            found += 1
+    assert found == 4
