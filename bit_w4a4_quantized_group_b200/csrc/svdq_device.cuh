@@ -102,19 +102,33 @@ __device__ __forceinline__ bool wait_bounded_call(uint64_t* bar, uint32_t parity
   return ptx::mbar_try_wait(ptx::smem_u32(bar), parity) || wait_bounded_loop(bar, parity, abort_flag, err, site);
 }
 
-// wait_bounded by a whole converged warp, with one result for all its lanes.  Each lane polls for itself, so
-// a barrier that completes just as the limit runs out may let some lanes pass and not others; lanes that part
-// there would meet again in an elect.sync or an .aligned instruction that names the whole warp, and wait
-// without a limit.  The vote makes every lane give up when one has.
-// The first poll is voted on by itself: where every lane passes there, as nearly always, nothing branches.
+// wait_bounded by a whole converged warp, with one result for all its lanes.  Lanes that polled each for
+// itself could part where a barrier completes just as the limit runs out, and meet again in an elect.sync or
+// an .aligned instruction that names the whole warp, to wait there without a limit.  So every poll and the
+// decision to give up are votes, and the warp never branches apart.
 __device__ __forceinline__ bool wait_bounded_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
                                                   int site, uint64_t limit_ns = kWaitLimitNs) {
-  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(ptx::smem_u32(bar), parity))) return true;
-  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err, site, limit_ns));
+  constexpr uint32_t kAll = 0xffffffffu;
+  const uint32_t a = ptx::smem_u32(bar);
+  if (__all_sync(kAll, ptx::mbar_try_wait(a, parity))) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  uint32_t spins = 0;
+  while (true) {
+    if (__all_sync(kAll, ptx::mbar_try_wait(a, parity))) return true;
+    if ((++spins & 63u) == 0) {
+      const bool aborted = *abort_flag != 0;
+      const bool late = !aborted && ptx::globaltimer() - t0 > limit_ns;
+      if (late) {
+        atomicCAS(err, 0, site);
+        *abort_flag = 1;
+      }
+      if (__any_sync(kAll, aborted || late)) return false;
+    }
+  }
 }
 static __device__ __noinline__ bool wait_bounded_loop_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                            int* err, int site) {
-  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err, site));
+  return wait_bounded_warp(bar, parity, abort_flag, err, site);
 }
 __device__ __forceinline__ bool wait_bounded_call_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                        int* err, int site) {
