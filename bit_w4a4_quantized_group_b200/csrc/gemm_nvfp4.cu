@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = j * ((nk_main + 1) / 2) + k / 2;
           const int ss = slot % kSfStages;
           const int b = mi % kSfBufs;
-          if (!wait_bounded(&sh->sf_full[ss], (slot / kSfStages) & 1, abort_flag, p.err, kErrSiteGemmFull) ||
-              !wait_bounded(&sh->sf_free[b], ((mi / kSfBufs) & 1) ^ 1u, abort_flag, p.err, kErrSiteGemmSfFree)) {
+          if (!wait_bounded_warp(&sh->sf_full[ss], (slot / kSfStages) & 1, abort_flag, p.err, kErrSiteGemmFull) ||
+              !wait_bounded_warp(&sh->sf_free[b], ((mi / kSfBufs) & 1) ^ 1u, abort_flag, p.err, kErrSiteGemmSfFree)) {
             ok = false;
             break;
           }
@@ -317,12 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id4 = idesc_nvf4(kBM, kBN);
       const uint32_t id16 = idesc_bf16(kBM, kBN);
       for (int j = 0; j < tiles.count && ok; ++j) {
-        if (!wait_bounded(&sh->acc_empty, acc_ph ^ 1u, abort_flag, p.err, kErrSiteGemmAccEmpty)) break;
+        if (!wait_bounded_warp(&sh->acc_empty, acc_ph ^ 1u, abort_flag, p.err, kErrSiteGemmAccEmpty)) break;
         ptx::tc_fence_after();
         for (int d = 0; d < nstg && ok; ++d, ++it) {
           const int s = it % kStages;
           const uint32_t ph = (it / kStages) & 1;
-          if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) {
+          if (!wait_bounded_warp(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) {
             ok = false;
             break;
           }
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int k = 2 * d + h2;
               if (k >= nk_main) break;
               const int b = mi % kSfBufs;
-              if (!wait_bounded(&sh->sf_ready[b], (mi / kSfBufs) & 1, abort_flag, p.err, kErrSiteGemmSfReady)) {
+              if (!wait_bounded_warp(&sh->sf_ready[b], (mi / kSfBufs) & 1, abort_flag, p.err, kErrSiteGemmSfReady)) {
                 ok = false;
                 break;
               }
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m0 = mb * kBM + static_cast<int>(rank) * kRows;
       const int col0 = nb * kBN + h * 128;
       const bool active = col0 < p.N;
-      if (!wait_bounded(&sh->acc_full, acc_ph, abort_flag, p.err, kErrSiteGemmAccFull)) break;
+      if (!wait_bounded_warp(&sh->acc_full, acc_ph, abort_flag, p.err, kErrSiteGemmAccFull)) break;
       ptx::tc_fence_after();
       // the whole 128-column slice into registers, then the accumulator goes back to the MMA
       // warp at once: the next tile's MMAs run while this one is scaled and stored

@@ -175,14 +175,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = it % kStages;
         const uint32_t ph = (it / kStages) & 1;
         ++it;
-        if (!wait_bounded(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) return 0xFFFFFFFFu;
+        if (!wait_bounded_warp(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) return 0xFFFFFFFFu;
         ptx::tc_fence_after();
         return static_cast<uint32_t>(s);
       };
       // Z L2^T of tile j added onto its converted accumulator
       auto branch = [&](int j) -> bool {
         const int b = j & 1;
-        if (!wait_bounded(&sh->conv_done[b], (j >> 1) & 1, abort_flag, p.err, kErrSiteGemmConvDone)) return false;
+        if (!wait_bounded_warp(&sh->conv_done[b], (j >> 1) & 1, abort_flag, p.err, kErrSiteGemmConvDone)) return false;
         ptx::tc_fence_after();
         for (int c = 0; c < nk_lr; ++c) {
           const uint32_t s = ring_wait();
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int j = 0; j < tiles.count && ok; ++j) {
         const int b = j & 1;
-        if (!wait_bounded(&sh->acc_empty[b], ((j >> 1) & 1) ^ 1u, abort_flag, p.err, kErrSiteGemmAccEmpty)) break;
+        if (!wait_bounded_warp(&sh->acc_empty[b], ((j >> 1) & 1) ^ 1u, abort_flag, p.err, kErrSiteGemmAccEmpty)) break;
         ptx::tc_fence_after();
         for (int k = 0; k < nk_main && ok; ++k) {
           const uint32_t s = ring_wait();
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           SVDQ_IN_GLOBAL(col0 + 128 <= p.N, p.err);
       const float sx = row < p.Mpad ? __ldg(sx_all + row) : 0.f;
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * 256 + h * 128;
-      if (!wait_bounded(&sh->acc_full[b], par, abort_flag, p.err, kErrSiteGemmAccFull)) break;
+      if (!wait_bounded_warp(&sh->acc_full[b], par, abort_flag, p.err, kErrSiteGemmAccFull)) break;
       ptx::tc_fence_after();
       if (lowrank) {
         // s32 -> fp32(acc) * (s_x s_w), in place, so that the branch MMAs can add onto it
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster(b ? conv_leader1 : conv_leader0);
-        if (!wait_bounded(&sh->acc_final[b], par, abort_flag, p.err, kErrSiteGemmAccFinal)) break;
+        if (!wait_bounded_warp(&sh->acc_final[b], par, abort_flag, p.err, kErrSiteGemmAccFinal)) break;
         ptx::tc_fence_after();
       }
       if (!active) {

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
     for (int it = 0; it < nit; ++it) {
       const int s = it % S;
       const uint32_t ph = (it / S) & 1;
-      if (!wait_bounded(&empty[s], ph ^ 1u, abort_flag, p.err, kErrSiteProEmpty)) break;
+      if (!wait_bounded_warp(&empty[s], ph ^ 1u, abort_flag, p.err, kErrSiteProEmpty)) break;
       const int ki = it % nkt;
       const bool with_l1 = RANK > 0 && it < nkt;      // L1 is only needed by the first pass
       const int kt = kbeg + (kt0 + ki) % nkt;
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
       const int it = pass * nkt + ki;
       const int s = it % S;
       const uint32_t ph = (it / S) & 1;
-      if (!wait_bounded(&full[s], ph, abort_flag, p.err, kErrSiteProFull)) { ok = false; break; }
+      if (!wait_bounded_warp(&full[s], ph, abort_flag, p.err, kErrSiteProFull)) { ok = false; break; }
       const int kt = kbeg + (kt0 + ki) % nkt;
       const int col0 = kt * BK + phase * 64;
       if (col0 < p.K &&
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
           for (int q = 0; q < p.ksplit; ++q)
             if (q != split) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(rm_bar), static_cast<uint32_t>(q)));
         }
-        if (!wait_bounded(rm_bar, 0u, abort_flag, p.err, kErrSiteProFull)) ok = false;
+        if (!wait_bounded_warp(rm_bar, 0u, abort_flag, p.err, kErrSiteProFull)) ok = false;
         ptx::fence_acq_rel_cluster();
         if (ok) {
           const uint32_t ra = ptx::smem_u32(rmax_cta + strip * 16 + g), rb2 = ptx::smem_u32(rmax_cta + strip * 16 + g + 8);
