@@ -8,6 +8,8 @@
 // overflows to infinity, whose reciprocal is 0, or underflows to 0 and leaves x.  exp and the
 // reciprocal are the hardware's approximations (2 and 1 units in the last place); the divide by
 // lambda shares the reciprocal, 1 / ((1 + exp(-t)) lambda).  All of it is far inside the E4M3 step of 2^-4.
+// A reciprocal below 2^-126 becomes 0 before up multiplies it: the interface states that, since a form
+// without it (the exponential halved and applied twice) would cost every element two more operations.
 //
 // What bounds it: memory (3 bytes per element, 5 with gating).  Eight lanes hold a group: a
 // thread has two 16-byte chunks of it (64 elements apart, so that the lanes of a load are

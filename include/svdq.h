@@ -249,7 +249,12 @@ svdq_status svdq_rmsnorm_quantize_act(svdq_format fmt, int64_t M, int64_t K,
  * gate and up are [M][K] with rows ldg and ldu elements apart (each >= K and a multiple of
  * 8), so that both may be column slices of one wider GEMM output; up NULL means no gating
  * (ldu is then ignored).  lambda is fp32 [K] as in svdq_quantize_act_lowrank_down, or NULL.
- * y is evaluated in fp32 with a relative error below 2^-15; values below 2^-110 may become 0.
+ * y is evaluated in fp32 from left to right as (gate f) [* up] with f = 1 / ((1 + exp(-t)) [lambda]),
+ * where act(x) = x / (1 + exp(-t)): t = x for SiLU, 2 sqrt(2/pi) (x + 0.044715 x^3) for GELU.  Its
+ * relative error is below 2^-15 as long as gate f and y are normal numbers.  Where 1 + exp(-t), or
+ * its product with lambda, is above 2^126, f may become 0 and y with it, whatever up and lambda are:
+ * SiLU gates below -87, GELU gates below -9.4, or lambda near the end of its range.  Without lambda and
+ * with |up| <= 2^9 that concerns values below 2^-110 only; smaller values of y may become 0 too.
  * The outputs feed svdq_w4a4_gemm_lowrank_up with rank 0.
  */
 svdq_status svdq_glu_quantize_act(svdq_format fmt, svdq_activation act, int64_t M, int64_t K,
