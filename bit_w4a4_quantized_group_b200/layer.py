@@ -80,10 +80,13 @@ class W4A4LowRankLinear:
                                  self.act_gscale, self.w_codes, self.w_scales, self.w_gscale,
                                  ws["Z"], self.L2, self.bias, Y, stream)
         if check:
-            st, site = B.svdq_get_last_device_error(torch.cuda.current_stream(self.device).cuda_stream)
-            if st != B.SVDQ_OK:
-                raise B.SvdqError(st, f"layer forward (device wait site {site})")
+            self._check_device("layer forward")
         return Y
+
+    def _check_device(self, what: str):
+        st, site = B.svdq_get_last_device_error(torch.cuda.current_stream(self.device).cuda_stream)
+        if st != B.SVDQ_OK:
+            raise B.SvdqError(st, f"{what} (device wait site {site})")
 
     def _input_rows(self, X: torch.Tensor) -> int:
         """M of a prologue's input, which the library reads as dense bf16 [M, K] on the current device."""
@@ -120,11 +123,12 @@ class W4A4LowRankLinear:
         return (g if self.lam is None else g / self.lam).contiguous()
 
     def forward_normed(self, X: torch.Tensor, residual: Optional[torch.Tensor], gamma: torch.Tensor, eps: float = 1e-6,
-                       H: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None) -> torch.Tensor:
+                       H: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+                       check: bool = False) -> torch.Tensor:
         """Y = the layer applied to RMSnorm(X + residual) * gamma, in two launches: the norm writes the
         layer's quantized input directly (fp8, rank 0).  `gamma` is fp32 [K] from fold_gamma (None: all
         ones, for a layer without smoothing); H, if given, receives X + residual in bf16 (it may be
-        `residual` or X itself).  Like forward(), asynchronous on the current stream."""
+        `residual` or X itself).  Like forward(), asynchronous on the current stream unless `check`."""
         self._check_fp8_feed("forward_normed")
         if gamma is None and self.lam is not None:
             raise ValueError("a layer with smoothing factors needs gamma from fold_gamma")
@@ -134,13 +138,15 @@ class W4A4LowRankLinear:
         ws = self.workspace(M)
         B.rmsnorm_quantize_act_t(self.fmt, X, residual, gamma, eps, H, ws["a_codes"], ws["a_scales"])
         self._gemm(M, Y)
+        if check:
+            self._check_device("layer forward_normed")
         return Y
 
     def forward_activated(self, act: str, gate: torch.Tensor, up: Optional[torch.Tensor] = None,
-                          Y: Optional[torch.Tensor] = None) -> torch.Tensor:
+                          Y: Optional[torch.Tensor] = None, check: bool = False) -> torch.Tensor:
         """Y = the layer applied to act(gate) [* up], in two launches: the second layer of an MLP on the
         first one's output (fp8, rank 0).  act is "silu" or "gelu" (tanh form); gate and up may be
-        column slices of one GEMM output."""
+        column slices of one GEMM output.  `check` as in forward()."""
         self._check_fp8_feed("forward_activated")
         self._check_width(gate, "gate")
         M = gate.shape[0]
@@ -148,6 +154,8 @@ class W4A4LowRankLinear:
         ws = self.workspace(M)
         B.glu_quantize_act_t(self.fmt, act, gate, up, self.lam, ws["a_codes"], ws["a_scales"])
         self._gemm(M, Y)
+        if check:
+            self._check_device("layer forward_activated")
         return Y
 
     def gemm_only(self, M: int, Y: torch.Tensor, rank: Optional[int] = None):

@@ -186,3 +186,23 @@ def test_hot_calls_take_the_streams_that_ctypes_takes():
                 with pytest.raises((TypeError, ctypes.ArgumentError)):
                     fn(*args, wrong)
     assert isinstance(torch.cuda.Stream._as_parameter_, property)
+
+
+def test_checked_calls_read_the_error_word(no_launch, monkeypatch):
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: B.SVDQ_OK
+    monkeypatch.setattr(B, "_calls", Library())
+    words = []
+    monkeypatch.setattr(B, "svdq_get_last_device_error", lambda stream: words.pop() if words else (B.SVDQ_OK, 0))
+    lin = _layer(128, 256)
+    X = torch.zeros((4, 256), dtype=torch.bfloat16)
+    for call in (lambda **kw: lin.forward(X, **kw), lambda **kw: lin.forward_normed(X, None, None, **kw),
+                 lambda **kw: lin.forward_activated("gelu", X, **kw)):
+        words[:] = [(B.SVDQ_ERR_TIMEOUT, 12)]
+        with pytest.raises(B.SvdqError, match="site 12"):
+            call(check=True)
+        assert not words
+        words[:] = [(B.SVDQ_ERR_TIMEOUT, 12)]
+        call()                                             # unchecked calls leave it for whoever polls it
+        assert words and call(check=False) is not None
