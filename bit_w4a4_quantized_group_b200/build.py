@@ -82,31 +82,41 @@ def _python_include() -> str:
     return inc if os.path.exists(os.path.join(inc, "Python.h")) else ""
 
 
-def _build_calls() -> None:
-    """The binding's extension.  Without Python's headers the binding goes through ctypes alone."""
-    inc = _python_include()
-    if not inc:
+def _build_calls(force: bool = False) -> None:
+    """The binding's extension, unless it is up to date.  It is optional: without Python's headers or a C
+    compiler that takes it the binding goes through ctypes alone, and an extension built from an older
+    source, whose calls need not match the library any more, is taken away."""
+    src = os.path.join(CSRC, "svdq_call.c")
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(
+            os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "svdq.h"))):
         return
-    tmp = CALLS + ".tmp"
-    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", inc, "-I", INCLUDE,
-           os.path.join(CSRC, "svdq_call.c"), "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for svdq_call.c:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    inc, why = _python_include(), "Python.h not found"
+    if inc:
+        tmp = CALLS + ".tmp"
+        try:
+            r = subprocess.run(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", inc, "-I", INCLUDE, src, "-o", tmp],
+                               capture_output=True, text=True)
+            if r.returncode == 0:
+                os.replace(tmp, CALLS)
+                return
+            why = r.stdout + r.stderr
+        except OSError as e:
+            why = str(e)
+    sys.stderr.write(f"svdq_call.so not built, the binding uses ctypes alone: {why}\n")
+    if os.path.exists(CALLS):
+        os.remove(CALLS)
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile every CUDA / C++ source of the library for sm_100a; return the .so path
     (the bounds-checking debug library when debug is true)."""
     lib = LIB_DEBUG if debug else LIB
-    if (not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime()
-            and (debug or os.path.exists(CALLS) or not _python_include())):
-        return lib
-    os.makedirs(BUILD_DEBUG if debug else BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     if not debug:
-        _build_calls()
+        _build_calls(force)
+    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime():
+        return lib
+    os.makedirs(BUILD_DEBUG if debug else BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose, debug), srcs))
