@@ -190,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph = 0, sfph = 0;
     const uint32_t id16 = idesc_bf16(kRowsW, T);
     const uint64_t desc0 = ptx::sdesc_sw128(ptx::smem_u32(smem));
-    const uint32_t sfx_skip = static_cast<uint32_t>(m0 & 127) / 32;    // T = 16 has m0 = 0
     for (int k = 0; k < nk + nk_lr; ++k) {
       if (!wait_bounded_call_warp(&sh->full[s], ph, abort_flag, p.err, kErrSiteGemmFull)) break;
       const bool main_step = k < nk;
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t xd = wd + kWBytes / 16;
         if (main_step) {
           const uint32_t sfa = tmem + C::kTmemSf0 + static_cast<uint32_t>(b) * 8;
-          const uint32_t sfb = sfa + 4 + sfx_skip;
+          const uint32_t sfb = sfa + 4;      // the tile starts its scale block: m0 is 0, or a multiple of 128 with T = 128
           const uint32_t idesc = idesc_mxf8(kRowsW, T) | (id << 29) | (id << 4);
 #pragma unroll
           for (int q = 0; q < kKTile / 32; ++q)
