@@ -254,7 +254,9 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
     // X and L1 seen as [K/64 column blocks][rows][64 columns]: one load brings kProBoxes (FP8: two, one
     // group) 64-column boxes (128B-swizzled) of 32 (FP8: 128 or 64) X rows or of all L1 rows
     const uint32_t boxes = fp8 ? 2 : kProBoxes;
-    const int rows = fp8 ? prologue_fp8_rows(p.M, p.K, device_sm_count(), &p.ksplit) : 32;
+    const int sms = fp8 ? device_sm_count() : 1;
+    if (sms <= 0) return SVDQ_ERR_CUDA;
+    const int rows = fp8 ? prologue_fp8_rows(p.M, p.K, sms, &p.ksplit) : 32;
     CUtensorMap tx, tl1;
     const uint64_t rs = static_cast<uint64_t>(K) * 2;
     if (!make_tmap_3d(&tx, X_bf16, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, M, K / 64, rs, 128, 64, rows, boxes,
