@@ -29,7 +29,7 @@ ACTIVATIONS = {"silu": SVDQ_ACT_SILU, "gelu": SVDQ_ACT_GELU_TANH}
 EXPORTED = (
     "svdq_buffer_sizes", "svdq_pack_weight", "svdq_quantize_act_lowrank_down",
     "svdq_w4a4_gemm_lowrank_up", "svdq_rmsnorm_quantize_act", "svdq_glu_quantize_act", "svdq_status_string", "svdq_get_last_device_error",
-    "svdq_last_launch_count", "svdq_last_cuda_error", "svdq_selftest_bounded_wait",
+    "svdq_last_launch_count", "svdq_last_variant", "svdq_last_cuda_error", "svdq_selftest_bounded_wait",
 )
 
 
@@ -70,6 +70,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.svdq_status_string.restype = ctypes.c_char_p
     lib.svdq_get_last_device_error.argtypes = [vp, ctypes.POINTER(c_int)]
     lib.svdq_last_launch_count.argtypes = []
+    lib.svdq_last_variant.argtypes = []
     lib.svdq_last_cuda_error.argtypes = []
     lib.svdq_last_cuda_error.restype = ctypes.c_char_p
     lib.svdq_selftest_bounded_wait.argtypes = [i64, vp]
@@ -162,6 +163,10 @@ def svdq_selftest_bounded_wait(limit_ns: int, stream=None) -> int:
 
 def svdq_last_launch_count() -> int:
     return load().svdq_last_launch_count()
+
+
+def svdq_last_variant() -> int:
+    return load().svdq_last_variant()
 
 
 def svdq_last_cuda_error() -> str:

@@ -347,7 +347,7 @@ int resident_clusters(int ks) {
 
 template <int T>
 cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw, const CUtensorMap& tsfx,
-                   const CUtensorMap& tl2, const CUtensorMap& tz, GemmParams p, cudaStream_t s) {
+                   const CUtensorMap& tl2, const CUtensorMap& tz, GemmParams p, cudaStream_t s, int* ksplit) {
   static_assert(smem_bytes<T>() <= 232448, "shared memory of one CTA");
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(gemm_fp8_small_kernel<T>), smem_bytes<T>());
   if (e != cudaSuccess) return e;
@@ -359,6 +359,7 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorM
       p.ksplit = ks;
       break;
     }
+  *ksplit = p.ksplit;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   // A ring no longer than a CTA's steps, and no deeper than 12 MB in flight over all CTAs need (1.5 us
@@ -397,12 +398,12 @@ int gemm_fp8_small_tokens(int M, int N, int K, int num_sms, float other_us) {
 
 cudaError_t launch_gemm_fp8_small(int tokens, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw,
                                   const CUtensorMap& tsfx, const CUtensorMap& tl2, const CUtensorMap& tz,
-                                  const GemmParams& p, cudaStream_t s) {
+                                  const GemmParams& p, cudaStream_t s, int* ksplit) {
   switch (tokens) {
-    case 16: return launch<16>(tw, tx, tsfw, tsfx, tl2, tz, p, s);
-    case 32: return launch<32>(tw, tx, tsfw, tsfx, tl2, tz, p, s);
-    case 64: return launch<64>(tw, tx, tsfw, tsfx, tl2, tz, p, s);
-    case 128: return launch<128>(tw, tx, tsfw, tsfx, tl2, tz, p, s);
+    case 16: return launch<16>(tw, tx, tsfw, tsfx, tl2, tz, p, s, ksplit);
+    case 32: return launch<32>(tw, tx, tsfw, tsfx, tl2, tz, p, s, ksplit);
+    case 64: return launch<64>(tw, tx, tsfw, tsfx, tl2, tz, p, s, ksplit);
+    case 128: return launch<128>(tw, tx, tsfw, tsfx, tl2, tz, p, s, ksplit);
   }
   return cudaErrorInvalidValue;
 }

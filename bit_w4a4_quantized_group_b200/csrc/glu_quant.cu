@@ -201,13 +201,14 @@ cudaError_t launch(const GluParams& p, int iters, const cudaLaunchConfig_t& cfg)
 
 }  // namespace
 
-cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s) {
+cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s, int* variant) {
   const int64_t cblocks = (p.K / 128 + kGroups - 1) / kGroups;
   // Four row pairs per CTA where that still leaves 3000 CTAs, four rounds of the device (GELU with lambda,
   // 4608 x 12288: 35.8 us against 37.6 with one and 37.2 with two; SiLU 8192 x 8192: 41.8 against 46.1;
   // 1000 rows of a small K get slower).  With gating a pair has twice the loads, and the next pair's
   // registers cost more than they give (SiLU with lambda, 8192 x 11008: 84.5 us against 77.8).
   const int iters = !p.up && cblocks * ((static_cast<int64_t>(p.M) + 2 * kIters - 1) / (2 * kIters)) >= 3000 ? kIters : 1;
+  *variant = iters;
   const int64_t rows = kRows * iters;
   const int64_t grid = cblocks * ((p.M + rows - 1) / rows) + (p.M % 128 ? 1 : 0);
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;

@@ -196,7 +196,7 @@ __global__ void __maxnreg__(VPT == 2 ? 52 : 40) rmsnorm_quant_kernel(NormParams 
 
 }  // namespace
 
-cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s) {
+cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s, int* variant) {
   // One unit per thread up to 256 threads, then two: with residual, 16384 x 3072 takes 54.9 us with 192
   // threads and 56.5 with 96, 8000 x 5120 47.7 us with 160 and 50.1 with 320, 4608 x 12288 64.3 us with 384
   // and 69.9 with 192 (four units).  Below 1024 rows, where a row's latency counts, one unit on up to 1024
@@ -204,6 +204,7 @@ cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s) {
   const int units = p.K / 16;
   int vpt = units <= (p.M < 1024 ? kMaxThreads : 256) ? 1 : 2;
   if ((units + vpt - 1) / vpt > kMaxThreads) vpt = 0;
+  *variant = vpt;
   const int threads = vpt > 0 ? ((units + vpt - 1) / vpt + 31) / 32 * 32 : kMaxThreads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.M) + (p.M % 128 ? 1u : 0u), 1, 1);

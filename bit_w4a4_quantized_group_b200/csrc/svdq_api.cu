@@ -21,6 +21,7 @@ __device__ int g_device_error = 0;   // the library's one piece of device state 
 namespace {
 
 thread_local int t_last_launch_count = 0;
+thread_local int t_last_variant = 0;
 thread_local cudaError_t t_last_cuda_error = cudaSuccess;
 
 svdq_status cuda_fail(cudaError_t e) {
@@ -189,6 +190,8 @@ extern "C" svdq_status svdq_buffer_sizes(svdq_format fmt, int64_t M, int64_t N, 
 
 extern "C" int svdq_last_launch_count(void) { return t_last_launch_count; }
 
+extern "C" int svdq_last_variant(void) { return t_last_variant; }
+
 extern "C" const char* svdq_last_cuda_error(void) { return cudaGetErrorName(t_last_cuda_error); }
 
 extern "C" svdq_status svdq_get_last_device_error(void* cuda_stream, int* site) {
@@ -208,7 +211,7 @@ extern "C" svdq_status svdq_get_last_device_error(void* cuda_stream, int* site) 
 }
 
 extern "C" svdq_status svdq_selftest_bounded_wait(int64_t limit_ns, void* cuda_stream) {
-  t_last_launch_count = 0;
+  t_last_launch_count = t_last_variant = 0;
   if (limit_ns < 1000 || limit_ns > 5000000000ll) return SVDQ_ERR_INVALID_ARG;
   int* err = device_error_word();
   if (!err) return SVDQ_ERR_CUDA;
@@ -223,7 +226,7 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
                                                       const void* X_bf16, const float* lambda, float act_gscale,
                                                       const void* L1_bf16, void* a_codes, void* a_scales,
                                                       void* Z_bf16, void* cuda_stream) {
-  t_last_launch_count = 0;
+  t_last_launch_count = t_last_variant = 0;
   svdq_status st = check_dims(fmt, M, 128, K, rank);
   if (st != SVDQ_OK) return st;
   if (!X_bf16 || !a_codes || !a_scales) return SVDQ_ERR_INVALID_ARG;
@@ -274,6 +277,7 @@ extern "C" svdq_status svdq_quantize_act_lowrank_down(svdq_format fmt, int64_t M
                    : fmt == SVDQ_FMT_W8A8      ? kFmtW8a8
                                                : kFmtInt4;
     e = fp8 ? launch_prologue_fp8(rows, tx, tl1, p, stream) : launch_prologue(kf, tx, tl1, p, stream);
+    if (fp8 && e == cudaSuccess) t_last_variant = 16 * rows + p.ksplit;
   }
   if (e != cudaSuccess) return cuda_fail(e);
   t_last_launch_count = 1;
@@ -285,7 +289,7 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
                                                  const void* w_codes, const void* w_scales, float w_gscale,
                                                  const void* Z_bf16, const void* L2_bf16, const void* bias_bf16,
                                                  void* Y_bf16, void* cuda_stream) {
-  t_last_launch_count = 0;
+  t_last_launch_count = t_last_variant = 0;
   svdq_status st = check_dims(fmt, M, N, K, rank);
   if (st != SVDQ_OK) return st;
   if (!a_codes || !a_scales || !w_codes || !w_scales || !Y_bf16) return SVDQ_ERR_INVALID_ARG;
@@ -380,8 +384,10 @@ extern "C" svdq_status svdq_w4a4_gemm_lowrank_up(svdq_format fmt, int64_t M, int
       tz = ta;
       tl2 = tb;
     }
-    e = small ? launch_gemm_fp8_small(small, tb, ta, tsfb, tsfa, tl2, tz, p, static_cast<cudaStream_t>(cuda_stream))
+    int ksplit = 0;
+    e = small ? launch_gemm_fp8_small(small, tb, ta, tsfb, tsfa, tl2, tz, p, static_cast<cudaStream_t>(cuda_stream), &ksplit)
               : launch_gemm_fp8(bn, ta, tb, tsfa, tsfb, tz, tl2, p, sms, static_cast<cudaStream_t>(cuda_stream));
+    if (e == cudaSuccess) t_last_variant = small ? -(16 * small + ksplit) : bn;
   } else if (fmt == SVDQ_FMT_W8A8) {
     p.tiles_m = static_cast<int>((M + 255) / 256);
     p.tiles_n = static_cast<int>((N + 255) / 256);
@@ -441,7 +447,7 @@ extern "C" svdq_status svdq_rmsnorm_quantize_act(svdq_format fmt, int64_t M, int
                                                  int64_t ldx, const void* residual_bf16, int64_t ldr,
                                                  const float* gamma, float eps, void* H_bf16, int64_t ldh,
                                                  void* a_codes, void* a_scales, void* cuda_stream) {
-  t_last_launch_count = 0;
+  t_last_launch_count = t_last_variant = 0;
   svdq_status st = check_dims(fmt, M, 128, K, 0);
   if (st != SVDQ_OK) return st;
   if (!good_rows(X_bf16, ldx, K) || (residual_bf16 && !good_rows(residual_bf16, ldr, K)))
@@ -470,8 +476,10 @@ extern "C" svdq_status svdq_rmsnorm_quantize_act(svdq_format fmt, int64_t M, int
   p.scales = static_cast<uint8_t*>(a_scales);
   p.err = device_error_word();
   if (!p.err) return SVDQ_ERR_CUDA;
-  cudaError_t e = launch_rmsnorm_quant(p, static_cast<cudaStream_t>(cuda_stream));
+  int variant = 0;
+  cudaError_t e = launch_rmsnorm_quant(p, static_cast<cudaStream_t>(cuda_stream), &variant);
   if (e != cudaSuccess) return cuda_fail(e);
+  t_last_variant = variant;
   t_last_launch_count = 1;
   return SVDQ_OK;
 }
@@ -480,7 +488,7 @@ extern "C" svdq_status svdq_glu_quantize_act(svdq_format fmt, svdq_activation ac
                                              const void* gate_bf16, int64_t ldg, const void* up_bf16, int64_t ldu,
                                              const float* lambda, void* a_codes, void* a_scales,
                                              void* cuda_stream) {
-  t_last_launch_count = 0;
+  t_last_launch_count = t_last_variant = 0;
   svdq_status st = check_dims(fmt, M, 128, K, 0);
   if (st != SVDQ_OK) return st;
   if (act != SVDQ_ACT_SILU && act != SVDQ_ACT_GELU_TANH) return SVDQ_ERR_INVALID_ARG;
@@ -502,8 +510,10 @@ extern "C" svdq_status svdq_glu_quantize_act(svdq_format fmt, svdq_activation ac
   p.scales = static_cast<uint8_t*>(a_scales);
   p.err = device_error_word();
   if (!p.err) return SVDQ_ERR_CUDA;
-  cudaError_t e = launch_glu_quant(p, static_cast<cudaStream_t>(cuda_stream));
+  int variant = 0;
+  cudaError_t e = launch_glu_quant(p, static_cast<cudaStream_t>(cuda_stream), &variant);
   if (e != cudaSuccess) return cuda_fail(e);
+  t_last_variant = variant;
   t_last_launch_count = 1;
   return SVDQ_OK;
 }

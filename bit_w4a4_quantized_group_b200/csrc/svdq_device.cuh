@@ -226,8 +226,9 @@ struct GluParams {
 int prologue_fp8_rows(int M, int K, int num_sms, int* ksplit);
 cudaError_t launch_prologue_fp8(int rows, const CUtensorMap& tx, const CUtensorMap& tl1, const ProParams& p, cudaStream_t s);
 cudaError_t launch_quantize_fp8(const void* X, const ProParams& p, cudaStream_t s);
-cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s);
-cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s);
+// *variant: what svdq_last_variant tells of the launch, as *ksplit below
+cudaError_t launch_rmsnorm_quant(const NormParams& p, cudaStream_t s, int* variant);
+cudaError_t launch_glu_quant(const GluParams& p, cudaStream_t s, int* variant);
 
 cudaError_t launch_prologue(int fmt, const CUtensorMap& tx, const CUtensorMap& tl1, const ProParams& p,
                             cudaStream_t s);
@@ -253,7 +254,7 @@ cudaError_t launch_gemm_fp8(int bn, const CUtensorMap& ta, const CUtensorMap& tb
 int gemm_fp8_small_tokens(int M, int N, int K, int num_sms, float other_us);
 cudaError_t launch_gemm_fp8_small(int tokens, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& tsfw,
                                   const CUtensorMap& tsfx, const CUtensorMap& tl2, const CUtensorMap& tz,
-                                  const GemmParams& p, cudaStream_t s);
+                                  const GemmParams& p, cudaStream_t s, int* ksplit);
 cudaError_t launch_gemm_int4(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tz,
                              const CUtensorMap& tl2, const CUtensorMap& ty, const CUtensorMap& tsa,
                              const CUtensorMap& tsb, const GemmParams& p, int num_sms, cudaStream_t s);

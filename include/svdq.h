@@ -288,6 +288,15 @@ svdq_status svdq_selftest_bounded_wait(int64_t limit_ns, void* cuda_stream);
 /* Number of kernels the last successful device call launched (for launch accounting). */
 int svdq_last_launch_count(void);
 
+/* Which variant of its kernel the last successful FP8 device call on this host thread launched, for tests
+ * and timings that have to reach each of them; the rules that choose stand at the launches and may change.
+ *   GEMM: the tile's columns (64, 128, 192, 256, 384); few tokens: -(16 * token tile + K split)
+ *   prologue with a branch: 16 * rows of a CTA + K split; without: 0
+ *   RMS norm: 16-element units of a thread (1, 2; 0 for rows wider than a CTA holds)
+ *   activation: row pairs of a CTA (1, 4)
+ * 0 after calls in other formats and after a call that failed. */
+int svdq_last_variant(void);
+
 /* Name of the CUDA runtime error behind the last SVDQ_ERR_CUDA returned on this
  * host thread ("cudaSuccess" if none). */
 const char* svdq_last_cuda_error(void);
