@@ -290,25 +290,14 @@ def _bfloat16():
     return _bf16
 
 
-_u8 = None
-
-
-def _uint8():
-    global _u8
-    if _u8 is None:
-        import torch
-        _u8 = torch.uint8
-    return _u8
-
-
 def _fp8_outputs(codes, scales, M, K, dev):
-    """Pointers of the buffers that a row operator writes: dense uint8 on that device, M K bytes for the
-    codes and ceil(M / 128) * 128 * ceil(K / 512) * 4 for the scales, or more."""
-    u8 = _u8 or _uint8()
-    if (codes.dtype is not u8 or codes.nbytes < M * K or codes.get_device() != dev or not codes.is_contiguous()
-            or scales.dtype is not u8 or scales.nbytes < (M + 127 >> 7) * (K + 511 >> 9) * 512
+    """Pointers of the buffers that a row operator writes: dense, of a one-byte type (uint8, or the float8 type
+    that the bytes stand for), on that device, M K bytes for the codes and
+    ceil(M / 128) * 128 * ceil(K / 512) * 4 for the scales, or more."""
+    if (codes.element_size() != 1 or codes.nbytes < M * K or codes.get_device() != dev or not codes.is_contiguous()
+            or scales.element_size() != 1 or scales.nbytes < (M + 127 >> 7) * (K + 511 >> 9) * 512
             or scales.get_device() != dev or not scales.is_contiguous()):
-        raise ValueError(f"a_codes, a_scales: expected contiguous uint8 of at least {M * K} and "
+        raise ValueError(f"a_codes, a_scales: expected contiguous uint8 (or float8) of at least {M * K} and "
                          f"{(M + 127 >> 7) * (K + 511 >> 9) * 512} elements on device {dev}, got "
                          f"{tuple(codes.shape)} {codes.dtype} on {codes.device} and {tuple(scales.shape)} "
                          f"{scales.dtype} on {scales.device}")
@@ -330,7 +319,7 @@ def _first_matrix(t, name):
 def rmsnorm_quantize_act_t(fmt, X, residual, gamma, eps, H, a_codes, a_scales, stream=None):
     """Residual addition + RMS norm + quantization on torch tensors: X, residual, H bf16 [M, K] (rows
     may be strided; residual and H may be None), gamma fp32 [K] or None.  a_codes and a_scales are dense
-    uint8, at least as long as svdq_buffer_sizes says."""
+    uint8 (or float8), at least as long as svdq_buffer_sizes says."""
     shape, dtype, dev, ldx = _first_matrix(X, "X")
     r = h = None
     ldr = ldh = 0

@@ -85,6 +85,15 @@ def test_row_helpers_take_buffers_of_the_stated_size(no_launch):
             B.glu_quantize_act_t("fp8", "silu", X, None, None, *buf)
 
 
+def test_row_helpers_take_buffers_of_the_float8_types_that_they_hold(no_launch):
+    X = torch.zeros((_M, _K), dtype=torch.bfloat16)
+    codes, scales = torch.zeros((_M, _K), dtype=torch.float8_e4m3fn), torch.zeros(_SCALES, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+    with pytest.raises(AssertionError, match="was called"):
+        B.rmsnorm_quantize_act_t("fp8", X, None, None, 1e-6, None, codes, scales)
+    with pytest.raises(AssertionError, match="was called"):
+        B.glu_quantize_act_t("fp8", "silu", X, None, None, codes, scales)
+
+
 def _layer(N, K):
     import numpy as np
     from bit_w4a4_quantized_group_b200 import prepare as P
