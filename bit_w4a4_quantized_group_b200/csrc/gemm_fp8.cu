@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+    end_issuing_role(abort_flag);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer (leader CTA only)
     // The whole warp runs the loop and the waits; one elected thread issues.
@@ -268,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    end_issuing_role(abort_flag);
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------ scale copier (leader CTA only)
     // Scale slot b goes to TMEM buffer b in both CTAs.  The producers refill the slot only when the
@@ -293,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++b == kSfBufs) { b = 0; sfph ^= 1u; }
       }
     }
+    end_issuing_role(abort_flag);
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ epilogue (8 warps, both CTAs)
     const int q = warp & 3;                 // TMEM lane quarter this warp may access
@@ -308,7 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned short touch = __ldg(reinterpret_cast<const unsigned short*>(p.bias) + col0 + lane * 64);
         asm volatile("" ::"h"(touch));
       }
-      if (!wait_bounded_warp(&sh->acc_full[a], use & 1u, abort_flag, p.err, kErrSiteGemmAccFull)) break;
+      if (!wait_bounded_warp(&sh->acc_full[a], use & 1u, abort_flag, p.err, kErrSiteGemmAccFull)) {
+        leave_aborted(abort_flag);
+        break;
+      }
       ptx::tc_fence_after();
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + a * BN + h * C::kColsPerWarp;
       const int row = m0 + q * 32 + lane;

@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+    end_issuing_role(abort_flag);
   } else if (warp == kCopyWarp) {
     // scale slot b -> TMEM buffer b; the producer refills the slot when the buffer is free
     int b = 0;
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (++b == kSfBufs) { b = 0; sfph ^= 1u; }
     }
+    end_issuing_role(abort_flag);
   } else if (warp == kMmaWarp) {
     int s = 0, b = 0;
     uint32_t ph = 0, sfph = 0;
@@ -220,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (sf_done && ++b == kSfBufs) { b = 0; sfph ^= 1u; }
       if (++s == stages) { s = 0; ph ^= 1u; }
     }
+    end_issuing_role(abort_flag);
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ thread = weight row, column = token
     const int q = warp & 3;
@@ -244,6 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             part[(c + e) * kRowsW] = __uint_as_float(v[e]);
       }
       ptx::tc_fence_before();
+    } else {
+      leave_aborted(abort_flag);
     }
     if (ks > 1) {
       // every other CTA gets its tokens' rows with one bulk copy
@@ -265,7 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();                                           // this CTA's own rows lie in its ring
   bool ok = *abort_flag == 0;
   if (ks > 1) {
-    ok = wait_bounded_call_warp(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
+    if (!wait_bounded_call_warp(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal)) {
+      ok = false;
+      leave_aborted(abort_flag);
+    }
     // what the others sent has arrived; when all CTAs say so, every copy has left its source
     __syncwarp();
     ptx::cluster_arrive();

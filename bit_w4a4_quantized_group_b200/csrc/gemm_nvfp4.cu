@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+    end_issuing_role(abort_flag);
   } else if (warp >= kCopyWarp0 && warp < kCopyWarp0 + kCopyWarps) {
     // ------------------------------------------------------------ scale copiers (leader CTA only)
     // Copy warp w moves blocks [w * per, (w + 1) * per) of every main step (A rows, and both row
@@ -308,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    end_issuing_role(abort_flag);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer (leader CTA only)
     if (rank == 0) {
@@ -377,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc_ph ^= 1u;
       }
     }
+    end_issuing_role(abort_flag);
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ epilogue (8 warps, both CTAs)
     const int q = warp & 3;                 // TMEM lane quarter this warp may access
@@ -384,12 +387,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t acc_empty_leader = ptx::mapa_shared(ptx::smem_u32(&sh->acc_empty), 0);
     const float sc = p.out_scale;
     uint32_t acc_ph = 0;
+    bool ok = true;
     for (int j = 0; j < tiles.count; ++j) {
       const int mb = tiles.mb(j), nb = tiles.nb(j);
       const int m0 = mb * kBM + static_cast<int>(rank) * kRows;
       const int col0 = nb * kBN + h * 128;
       const bool active = col0 < p.N;
-      if (!wait_bounded_warp(&sh->acc_full, acc_ph, abort_flag, p.err, kErrSiteGemmAccFull)) break;
+      if (!wait_bounded_warp(&sh->acc_full, acc_ph, abort_flag, p.err, kErrSiteGemmAccFull)) { ok = false; break; }
       ptx::tc_fence_after();
       // the whole 128-column slice into registers, then the accumulator goes back to the MMA
       // warp at once: the next tile's MMAs run while this one is scaled and stored
@@ -448,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (!ok) leave_aborted(abort_flag);
   }
 
   // Both CTAs finished: every MMA has completed (each epilogue saw its last

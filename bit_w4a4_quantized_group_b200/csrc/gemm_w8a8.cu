@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < nk_lr && ok; ++c) ok = step(tiles.count - 1, -1 - c);
     }
     __syncwarp();
+    end_issuing_role(abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader CTA only)
     if (rank == 0) {
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok && tiles.count > 0 && nk_lr > 0) branch(tiles.count - 1);
     }
+    end_issuing_role(abort_flag);
   } else {
     // ------------------------------------------------------------ epilogue (warps 2-9, both CTAs)
     const int q = warp & 3;                 // TMEM lane quarter this warp may access
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float* sx_all = reinterpret_cast<const float*>(p.a_scales);
     uint8_t* buf = epi_smem + (warp - kEpiWarp0) * kEpiBoxBytes;
     const bool lowrank = nk_lr > 0;
+    bool ok = true;
     for (int j = 0; j < tiles.count; ++j) {
       const int b = j & 1;
       const uint32_t par = (j >> 1) & 1;
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           SVDQ_IN_GLOBAL(col0 + 128 <= p.N, p.err);
       const float sx = row < p.Mpad ? __ldg(sx_all + row) : 0.f;
       const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * 256 + h * 128;
-      if (!wait_bounded_warp(&sh->acc_full[b], par, abort_flag, p.err, kErrSiteGemmAccFull)) break;
+      if (!wait_bounded_warp(&sh->acc_full[b], par, abort_flag, p.err, kErrSiteGemmAccFull)) { ok = false; break; }
       ptx::tc_fence_after();
       if (lowrank) {
         // s32 -> fp32(acc) * (s_x s_w), in place, so that the branch MMAs can add onto it
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster(b ? conv_leader1 : conv_leader0);
-        if (!wait_bounded_warp(&sh->acc_final[b], par, abort_flag, p.err, kErrSiteGemmAccFinal)) break;
+        if (!wait_bounded_warp(&sh->acc_final[b], par, abort_flag, p.err, kErrSiteGemmAccFinal)) { ok = false; break; }
         ptx::tc_fence_after();
       }
       if (!active) {
@@ -347,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) ptx::bulk_wait_group<0>();
     __syncwarp();
+    if (!ok) leave_aborted(abort_flag);
   }
 
   // Both CTAs finished: every MMA has completed (each epilogue saw its last accumulator)

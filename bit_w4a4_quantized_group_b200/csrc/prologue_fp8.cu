@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       ptx::mbar_arrive(&sh->full[s]);        // each lane releases its own stores
       if (++s == S) { s = 0; ph ^= 1u; }
     }
+    end_issuing_role(abort_flag);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ Z += X_hat L1^T
     int s = 0;
@@ -318,6 +319,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       __syncwarp();
       if (++s == S) { s = 0; ph ^= 1u; }
     }
+    end_issuing_role(abort_flag);
   } else {
     // ------------------------------------------------------------ compute warps
     // Two sets of eight warps take the tiles in turn, so that one set's waits and stores overlap the
@@ -330,7 +332,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     int s = set % S;
     uint32_t ph = static_cast<uint32_t>(set / S) & 1u;
     for (int g = set; g < ng; g += 2) {
-      if (!wait_bounded_warp(&sh->full[s], ph, abort_flag, p.err, kErrSiteProFull)) break;
+      if (!wait_bounded_warp(&sh->full[s], ph, abort_flag, p.err, kErrSiteProFull)) {
+        leave_aborted(abort_flag);
+        break;
+      }
       uint8_t* st = smem + s * stage;
       Divisors d;
       if (LAM) {
@@ -411,6 +416,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                                    __uint_as_float(z[4 * e + 2]), __uint_as_float(z[4 * e + 3]));
         }
         ptx::tc_fence_before();
+      } else {
+        leave_aborted(abort_flag);
       }
       if (ks > 1) {
         // every other CTA gets its rows with one bulk copy
@@ -434,7 +441,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   __syncthreads();
   bool ok = *abort_flag == 0;
   if (ks > 1) {
-    ok = wait_bounded_warp(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal) && ok;
+    if (!wait_bounded_warp(&sh->red_full, 0u, abort_flag, p.err, kErrSiteGemmAccFinal)) {
+      ok = false;
+      leave_aborted(abort_flag);
+    }
     // what the others sent has arrived; when all CTAs say so, every copy has left its source
     __syncwarp();
     ptx::cluster_arrive();

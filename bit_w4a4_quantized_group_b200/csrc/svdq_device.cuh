@@ -31,6 +31,7 @@ enum : int {
   kErrSiteGemmAccFinal = 20,
   kErrSiteSelftest = 90,
   kErrSiteSelftestParted = 91,
+  kErrSiteSelftestPeer = 92,
   // Debug builds (-DSVDQ_DEBUG) only: an access outside its buffer was found and skipped.
   kErrSiteBoundsGlobal = 201,   // a plain global load or store past its buffer
   kErrSiteBoundsShared = 202,   // a shared-memory access past the dynamic allocation
@@ -68,6 +69,23 @@ __device__ __forceinline__ bool smem_in_bounds(const void* base, const void* p, 
 // A wait gives up after this many nanoseconds (~1 s); legitimate waits here
 // last microseconds.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
+
+// After an abort.  Copies and MMAs may still be on their way through the shared and tensor memory of the
+// cluster's CTAs with nobody left who waits for them; they take a few microseconds.  So a role whose wait ran
+// out, and a role that issued any and finds the flag raised when it ends, tells the other CTAs of the cluster
+// and stays for a thousand microseconds before it goes on to the CTA's or cluster's last barrier.  Whatever was
+// issued before an abort is covered by the role that aborted, whatever was issued behind it by the role that
+// issued it; without an abort every copy and MMA has a waiter as before.
+constexpr uint64_t kDrainNs = 1000000ull;
+static __device__ __noinline__ void leave_aborted(volatile int* abort_flag) {
+  const uint32_t a = ptx::smem_u32(const_cast<const int*>(abort_flag)), n = ptx::cluster_nctarank();
+  for (uint32_t r = 0; r < n; ++r) ptx::st_shared_cluster_u32(ptx::mapa_shared(a, r), 1u);
+  const uint64_t t0 = ptx::globaltimer();
+  while (ptx::globaltimer() - t0 < kDrainNs) __nanosleep(2000);
+}
+__device__ __forceinline__ void end_issuing_role(volatile int* abort_flag) {
+  if (__builtin_expect(*abort_flag != 0, 0)) leave_aborted(abort_flag);
+}
 
 // Parity wait on an mbarrier with a time limit.  On time-out the first waiter
 // records its site in the device error word, raises the CTA's abort flag and

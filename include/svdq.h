@@ -278,7 +278,9 @@ svdq_status svdq_get_last_device_error(void* cuda_stream, int* site);
  * at, with the same bounded wait the kernels use but a limit of limit_ns
  * nanoseconds (1e3 <= limit_ns <= 5e9); half of its lanes ask for a phase that has
  * completed, and have to give up with the others.  The wait runs out, the kernel records
- * site 90 in the device error word (91: the lanes parted) and returns, leaving the context usable; a
+ * site 90 in the device error word (91: the lanes parted; 92: the other CTA of its cluster was not
+ * told), keeps its memory for 1 ms more as every kernel does after an abort, and returns, leaving the
+ * context usable; a
  * following svdq_get_last_device_error returns SVDQ_ERR_TIMEOUT with *site == 90.
  * Returns SVDQ_ERR_INVALID_ARG for a limit out of range, SVDQ_ERR_CUDA if the
  * launch fails.

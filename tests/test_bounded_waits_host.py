@@ -81,3 +81,45 @@ def test_barriers_in_aligned_form_gather_the_warp_first():
             assert "__syncwarp();" in body, (name, text.count("\n", 0, m.start()) + 1)
             found += 1
     assert found == 4
+
+
+def _roles(kernel):
+    """(start, end) of the blocks of a kernel's roles: the branches on the warp that hold waits."""
+    out, stack = [], []
+    for m in re.finditer(r"[{}]", kernel):
+        if m.group() == "{":
+            head = kernel[max(kernel.rfind(c, 0, m.start()) for c in ";{}") + 1: m.start()]
+            chained = bool(re.search(r"\belse\s*$", head)) and bool(out) and kernel[out[-1][1]: m.start()].strip() == "else"
+            stack.append((m.end(), chained or bool(re.search(r"if \((warp|first)\b[^{;]*$", head))))
+        else:
+            start, role = stack.pop()
+            if role and not any(r for _, r in stack):
+                out.append((start, m.end()))
+    return [(a, b) for a, b in out if "wait_bounded" in kernel[a: b]]
+
+
+@pytest.mark.parametrize("name,roles", [("gemm_fp8.cu", 4), ("gemm_fp8_small.cu", 4), ("prologue_fp8.cu", 3), ("gemm_nvfp4.cu", 4),
+                                        ("gemm_w8a8.cu", 3), ("gemm_int4.cu", 4), ("prologue.cu", 2), ("selftest.cu", 1)])
+def test_roles_stay_for_their_copies_after_an_abort(name, roles):
+    """A role that issues copies or MMAs looks at the abort flag when it ends; one that does not stays where its
+    own wait ran out; and so does a wait outside of the roles, before the next barrier."""
+    with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    starts = [m.start() for m in re.finditer(r"__global__ void ", text)] + [len(text)]
+    kernels = [k for k in (text[a: b] for a, b in zip(starts, starts[1:])) if "wait_bounded" in k]
+    assert len(kernels) == 1
+    kernel = kernels[0][kernels[0].index("{"):]
+    kernel = kernel[: re.search(r"\n}\n", kernel).end()]
+    found = _roles(kernel)
+    assert len(found) == roles
+    for a, b in found:
+        role = kernel[a: b]
+        last = role.rindex("wait_bounded")
+        if re.search(r"tma_load|umma_|tmem_cp", role):
+            assert "end_issuing_role(abort_flag);" in role[last:], role[:200]
+        else:
+            assert len(re.findall(r"wait_bounded", role)) >= 1 and "leave_aborted(" in role[last:], role[:200]
+    for m in re.finditer(r"wait_bounded", kernel):
+        if not any(a <= m.start() < b for a, b in found):
+            rest = kernel[m.start():]
+            assert rest.index("leave_aborted(abort_flag)") < re.search(r"cluster_|__syncthreads", rest).start()
