@@ -29,7 +29,9 @@
 //     accumulator;
 //   * eight epilogue warps per CTA drain TMEM into registers, hand the accumulator back, add the
 //     bias and store bf16 Y while the next tile's MMAs run.  192 columns and fewer leave TMEM for
-//     two accumulators, so that the next tile's MMAs do not wait for the drain either.
+//     two accumulators, so that the next tile's MMAs do not wait for the drain either; 256 and 384
+//     columns have one, whose drain the MMAs wait for.
+// Sizes in comments are M x K x N.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -373,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           store(o, c16 * 16);
         }
       } else {
-        // 192 columns: as bf16 pairs, since the registers do not hold that many fp32 values
+        // 192 columns: as bf16 pairs, since the registers do not hold that many fp32 values; even so this
+        // kernel spills 136 bytes a thread (168 registers), the narrower ones nothing
         uint32_t o[2 * NC][8];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -468,7 +471,9 @@ float gemm_fp8_tile(int M, int N, int K, int num_sms, int* bn) {
   // of a step, 0.13 us + 1.53 ns per column, and 4 us to start and drain.  Measured back to back, us a
   // step for widths 384, 256, 192, 128 and 64: 0.75, 0.54, 0.43, 0.32 and 0.23 at 4608 x 12288 x 3072;
   // whole calls 7.8 us at 300 x 2176 x 1152 (64 wide), 12.0 at 256 x 3072 x 9216 (128), 12.9 at 1024 x
-  // 3072 x 3072 (192), 22.9 at 2048 x 3072 x 3072 (384; 24.9 with 256).
+  // 3072 x 3072 (192), 22.9 at 2048 x 3072 x 3072 (384; 24.9 with 256).  The rule knows neither a tile's
+  // drain nor the bytes of Y: both 4608-token products come out at 142 us (141 measured for K = 12288, 157
+  // for N = 12288), and with a single K step it is far off (16384 x 128 x 12288: 24 us, 155 measured).
   const int64_t tm = (M + kBM - 1) / kBM;
   const int64_t slots = num_sms / 2 > 0 ? num_sms / 2 : 1;
   float best = 0.f;

@@ -11,6 +11,11 @@
 //
 // Scales: as in gemm_fp8.cu a 512-byte block serves four K steps and has a ring of its own; a CTA
 // whose share starts inside such a block loads that block with its first step.
+//
+// What bounds it: reading the weights, and the 4 us around that.  1 x 3072 x 9216 (M x K x N, here and below)
+// takes 7.0 us with its 28 MB of weights in L2 and 8.1 with weights from HBM, which need 4.4; 64 x 3072 x
+// 12288 10.9 and 11.5, where 5.9 would do: 96 tiles leave no second CTA for each, so that K is not split and
+// 52 SMs have no work.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <atomic>
@@ -386,8 +391,8 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorM
 }  // namespace
 
 int gemm_fp8_small_tokens(int M, int N, int K, int num_sms, float other_us) {
-  // Up to 64 tokens this kernel is the faster one (one token x 3072 x 9216: 7.7 us against 12; 64 x
-  // 3072 x 12288: 12.4 against 14).  Beyond, tiles of 128 tokens pay where the other kernel has few
+  // Up to 64 tokens this kernel is the faster one (1 x 3072 x 9216: 7.7 us against 12; 64 x 3072 x 12288:
+  // 12.4 against 14).  Beyond, tiles of 128 tokens pay where the other kernel has few
   // tiles and a long K: 4.3 us and 25 ns per token of a tile to start, add up and drain, and per K step 0.22 us or the time of
   // 32 KB for every CTA at 8.6 TB/s (us measured, this kernel / the other: 128 x 12288 x 3072 15.9 / 26,
   // 512 x 8192 x 512 10.9 / 19, 512 x 3072 x 9216 42 / 17).

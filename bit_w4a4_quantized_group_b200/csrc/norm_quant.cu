@@ -7,9 +7,10 @@
 // element with a residual, 3 without.  One CTA holds one row in registers as bf16, adds the squares
 // over the CTA, and quantizes from the registers: no second read.  Eight lanes hold a group of 128,
 // two 16-byte chunks each, 64 elements apart so that the lanes of a load are neighbours; products run
-// on pairs (f32x2).  Before, 16 lanes held a group, with one chunk each and scalar products: the
-// shuffles, scale bytes and scalar products of twice as many lanes cost 56.9 us for 16384 x 3072 with
-// residual (now 54.9) and 80.2 us for 4608 x 12288 (now 64.3).  Forming h gamma and the maxima before
+// on pairs (f32x2).  Sixteen lanes to a group, with one chunk each and scalar products, take 56.9 us for
+// 16384 x 3072 with residual against 54.9, and 80.2 us for 4608 x 12288 (rows x K here and below) against
+// 64.3: twice as many lanes do shuffles and scale bytes.  Without a residual 4608 x 12288 takes 37 us where
+// its bytes take 26: nothing is loaded while a CTA sums and quantizes its row.  Forming h gamma and the maxima before
 // the CTA's sum is known saves work behind the barrier but keeps twice the registers: 60.2 and 66.5 us.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -21,9 +21,10 @@
 // What bounds them.  Without a branch memory, 3 bytes per element: 16384 x 3072 takes 24.1 us (6.3 TB/s).
 // The instructions around the codes decide how near it comes (8.6 per element; 11.8 took 29.5 us), so
 // maxima are taken on bf16 pairs, two rows at a time, and one offset serves all of a thread's rows.
-// With a branch the 16 compute warps of an SM: 4608 x 3072, rank 32, takes 14.6 us, of which 2.4 pass
+// With a branch the latency of a tile's way through the ring (TMA, shared memory to registers and back, MMA)
+// with one CTA of 16 compute warps on an SM: 4608 x 3072 (rows x K), rank 32, takes 14.3 us, of which 2.4 pass
 // before the first tile is there and 1.5 in the cluster's exchange; a tile of 64 rows takes 0.77 us, where
-// its bytes would take 0.56.  24 warps in three sets (15.4 us), eight lanes to a group (15.8) and more
+// its bytes would take 0.56, with issue slots 41% busy.  24 warps in three sets (15.4 us), eight lanes to a group (15.8) and more
 // stages (14.6) give nothing there.
 //
 // The divide.  X_hat = bf16(RN_f32(x / lambda)) is formed as bf16(q), q = fma(x, yh, x yl), with
