@@ -34,6 +34,7 @@
 // Sizes in comments are M x K x N.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -410,7 +411,7 @@ size_t smem_bytes() {
 
 template <int BN>
 int max_active_clusters(size_t smem) {
-  static int cache[64] = {0};
+  static std::atomic<int> cache[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];

@@ -42,6 +42,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -574,7 +575,7 @@ namespace {
 // the current device (0 if none or on error), queried once per device and split size.
 int int4_resident_clusters(int ks, size_t smem) {
   constexpr int kDevs = 64;
-  static int cached[kDevs][9];            // 0: not queried yet, else 1 + the figure
+  static std::atomic<int> cached[kDevs][9];   // 0: not queried yet, else 1 + the figure
   int dev = 0;
   if (ks < 2 || ks > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return 0;
   if (cached[dev][ks] > 0) return cached[dev][ks] - 1;

@@ -51,6 +51,7 @@
 //     per warp instruction).
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool MX>
 int max_active_clusters(size_t smem) {
-  static int cache[64] = {0};
+  static std::atomic<int> cache[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];

@@ -25,6 +25,7 @@
 //     Y through 128B-swizzled staging and TMA stores.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 size_t smem_bytes() { return 1024 + kStages * kStageBytes + kEpiWarps * kEpiBoxBytes + sizeof(SharedTail); }
 
 int max_active_clusters(size_t smem) {
-  static int cache[64] = {0};
+  static std::atomic<int> cache[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];

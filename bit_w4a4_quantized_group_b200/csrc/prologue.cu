@@ -47,6 +47,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "ptx.cuh"
@@ -695,8 +696,8 @@ int stages_for() {
 template <int FMT, int RANK>
 static int resident_clusters(int ks, size_t smem) {
   constexpr int kDevs = 64;
-  static int cached[kDevs][9];            // 0: not queried yet, else 1 + the figure
-  static size_t cached_smem[kDevs][9];
+  static std::atomic<int> cached[kDevs][9];   // 0: not queried yet, else 1 + the figure
+  static std::atomic<size_t> cached_smem[kDevs][9];
   int dev = 0;
   if (ks < 2 || ks > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return 0;
   if (cached[dev][ks] > 0 && cached_smem[dev][ks] == smem) return cached[dev][ks] - 1;

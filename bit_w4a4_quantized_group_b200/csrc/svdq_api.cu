@@ -120,7 +120,7 @@ namespace {
 int device_sm_count() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  static int cache[64] = {0};
+  static std::atomic<int> cache[64];
   if (dev < 0 || dev >= 64) return 0;
   if (cache[dev] == 0) {
     int n = 0;
