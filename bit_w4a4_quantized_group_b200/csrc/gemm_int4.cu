@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-    end_issuing_role(abort_flag);
+    end_issuing_role_of_cta(abort_flag);
   } else if (warp < kLoadWarps) {
     // ------------------------------------------------------------ widening warps
     // Every lane waits and arrives for itself and the warp does nothing together, so that its lanes may
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!ok) leave_aborted(abort_flag);
+    if (!ok) stay_after_abort();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     int it = 0, gi = 0, li = 0;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++gi;
     }
-    end_issuing_role(abort_flag);
+    end_issuing_role_of_cta(abort_flag);
   } else {
     // ------------------------------------------------------------ epilogue (warps 4-11)
     // Each warp owns 32 rows (its TMEM lane quarter) x 64 columns and reads them in the
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) ptx::bulk_wait_group<0>();
     __syncwarp();
-    if (!ok) leave_aborted(abort_flag);
+    if (!ok) stay_after_abort();
   }
 
   if (SPLIT) {

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
       }
       ptx::mbar_arrive(&full[s]);   // each lane releases its own lambda stores
     }
-    end_issuing_role(abort_flag);
+    end_issuing_role_of_cta(abort_flag);
   } else {
     // ---------------------------------------------------------------- compute warps
     const int strip = warp & 1;         // rows 16*strip .. 16*strip+15 of the CTA tile
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(32 * (compute_warps(RANK) + 1), 1)
         }
       }
     }
-    if (!ok) leave_aborted(abort_flag);
+    if (!ok) stay_after_abort();
   }
 
   // K split over a cluster: CTA 0 adds the other CTAs' Z partials (read through distributed

@@ -77,14 +77,24 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;
 // issued before an abort is covered by the role that aborted, whatever was issued behind it by the role that
 // issued it; without an abort every copy and MMA has a waiter as before.
 constexpr uint64_t kDrainNs = 1000000ull;
-static __device__ __noinline__ void leave_aborted(volatile int* abort_flag) {
-  const uint32_t a = ptx::smem_u32(const_cast<const int*>(abort_flag)), n = ptx::cluster_nctarank();
-  for (uint32_t r = 0; r < n; ++r) ptx::st_shared_cluster_u32(ptx::mapa_shared(a, r), 1u);
+//
+// Kernels whose copies and MMAs stay within a CTA stay without telling: their CTAs need not end together, and a
+// CTA that has ended must not be written to.
+__device__ __forceinline__ void stay_after_abort_inline() {
   const uint64_t t0 = ptx::globaltimer();
   while (ptx::globaltimer() - t0 < kDrainNs) __nanosleep(2000);
 }
+static __device__ __noinline__ void stay_after_abort() { stay_after_abort_inline(); }
+static __device__ __noinline__ void leave_aborted(volatile int* abort_flag) {
+  const uint32_t a = ptx::smem_u32(const_cast<const int*>(abort_flag)), n = ptx::cluster_nctarank();
+  for (uint32_t r = 0; r < n; ++r) ptx::st_shared_cluster_u32(ptx::mapa_shared(a, r), 1u);
+  stay_after_abort_inline();
+}
 __device__ __forceinline__ void end_issuing_role(volatile int* abort_flag) {
   if (__builtin_expect(*abort_flag != 0, 0)) leave_aborted(abort_flag);
+}
+__device__ __forceinline__ void end_issuing_role_of_cta(volatile int* abort_flag) {
+  if (__builtin_expect(*abort_flag != 0, 0)) stay_after_abort();
 }
 
 // Parity wait on an mbarrier with a time limit.  On time-out the first waiter

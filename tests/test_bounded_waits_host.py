@@ -116,10 +116,17 @@ def test_roles_stay_for_their_copies_after_an_abort(name, roles):
         role = kernel[a: b]
         last = role.rindex("wait_bounded")
         if re.search(r"tma_load|umma_|tmem_cp", role):
-            assert "end_issuing_role(abort_flag);" in role[last:], role[:200]
+            assert re.search(r"end_issuing_role(_of_cta)?\(abort_flag\);", role[last:]), role[:200]
         else:
-            assert len(re.findall(r"wait_bounded", role)) >= 1 and "leave_aborted(" in role[last:], role[:200]
+            assert re.search(r"leave_aborted\(|stay_after_abort\(", role[last:]), role[:200]
     for m in re.finditer(r"wait_bounded", kernel):
         if not any(a <= m.start() < b for a, b in found):
             rest = kernel[m.start():]
             assert rest.index("leave_aborted(abort_flag)") < re.search(r"cluster_|__syncthreads", rest).start()
+    # a CTA of the cluster that has ended must not be told: only where all of them meet at the end, always
+    tells = re.search(r"leave_aborted\(|end_issuing_role\(", kernel)
+    meets = kernel[kernel.rindex("cluster_"):] if "cluster_" in kernel else ""
+    assert bool(tells) == (name not in ("prologue.cu", "gemm_int4.cu"))
+    if tells:
+        line = kernel[: kernel.rindex("cluster_")].split("\n")[-1]
+        assert meets.startswith(("cluster_sync();", "cluster_wait();")) and line.strip() in ("ptx::", "if (ks > 1) ptx::"), line
